@@ -487,6 +487,159 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
   return attn_dispatch(D, S2, t->q, stg + L.k_off, stg + L.v_off, sel_st, t->out, workspace, workspace_bytes, st);
 }
 
+// ---------------------------------------------------------------- paged cache
+namespace {
+// The sizes of a paged batch; the device pointers are checked where they are used.
+qsa_status_t resolve_paged(const qsa_paged_t *pg, Paged *G) {
+  if (!pg) return QSA_ERR_INVALID_ARG;
+  if (pg->batch < 0 || pg->n_tok < 0 || pg->max_chunk < 0 || pg->n_pages < 0 || pg->max_pages < 0)
+    return QSA_ERR_INVALID_ARG;
+  const int ps = pg->page_size;
+  if (ps <= 0 || (ps & (ps - 1)) != 0) return QSA_ERR_INVALID_ARG;
+  if (ps < 16 || ps > 32768) return QSA_ERR_UNSUPPORTED;
+  if (pg->batch > 0 && pg->n_tok > 0 && (pg->max_chunk == 0 || pg->n_pages == 0 || pg->max_pages == 0))
+    return QSA_ERR_INVALID_ARG;
+  G->q_start = pg->q_start;
+  G->kv_len = pg->kv_len;
+  G->table = pg->page_table;
+  G->batch = pg->batch;
+  G->n_tok = pg->n_tok;
+  G->max_chunk = pg->max_chunk < pg->n_tok ? pg->max_chunk : pg->n_tok;
+  G->ps = ps;
+  G->ps_shift = 0;
+  while ((1 << G->ps_shift) < ps) ++G->ps_shift;
+  G->n_pages = pg->n_pages;
+  G->max_pages = pg->max_pages;
+  return QSA_OK;
+}
+
+// Norm and rotation parameters; nr NULL: rows are copied as they are.
+qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRope *N) {
+  *N = NormRope{};
+  if (!nr) return QSA_OK;
+  if (!(nr->eps >= 0.f) || !(nr->weight_offset == nr->weight_offset)) return QSA_ERR_INVALID_ARG;
+  if (nr->rotary_dim < 0 || nr->rotary_dim % 16 != 0 || nr->rotary_dim > D.d || nr->indexer_rotary_dim < 0 ||
+      nr->indexer_rotary_dim % 16 != 0 || nr->indexer_rotary_dim > D.di)
+    return QSA_ERR_INVALID_ARG;
+  if ((nr->rotary_dim || nr->indexer_rotary_dim) && !(nr->rope_theta >= 1.f && nr->rope_theta <= 3.0e38f))
+    return QSA_ERR_INVALID_ARG;
+  if (!aligned16(nr->q_weight) || !aligned16(nr->k_weight)) return QSA_ERR_INVALID_ARG;
+  N->eps = nr->eps;
+  N->w_off = nr->weight_offset;
+  N->log2_theta = nr->rotary_dim || nr->indexer_rotary_dim ? log2((double)nr->rope_theta) : 0.0;
+  N->rot = nr->rotary_dim;
+  N->rot_i = nr->indexer_rotary_dim;
+  N->qw = nr->q_weight;
+  N->kw = nr->k_weight;
+  return QSA_OK;
+}
+
+// A packed tensor of rows of `width` elements, `row` elements apart.
+bool rows_ok(const Dims &D, const void *p, long long row, long long width) {
+  return p && aligned16(p) && row >= width && row % (D.bf16 ? 8 : 4) == 0;
+}
+}  // namespace
+
+qsa_status_t qsa_norm_rope(const qsa_config_t *cfg, const qsa_norm_rope_t *nr, const int32_t *pos, int32_t n_tok,
+                           const void *q, int64_t q_row, void *q_out, int64_t q_out_row, const void *k, int64_t k_row,
+                           void *k_out, int64_t k_out_row, qsa_stream_t stream) {
+  g_serial_at_entry = g_error_serial;
+  Dims D;
+  NormRope N;
+  qsa_status_t s = resolve(cfg, &D);
+  if (s != QSA_OK) return s;
+  if (!nr || n_tok < 0) return QSA_ERR_INVALID_ARG;
+  if ((s = resolve_norm_rope(D, nr, &N)) != QSA_OK) return s;
+  if (n_tok == 0 || (!q && !k)) return QSA_OK;
+  if (!pos) return QSA_ERR_INVALID_ARG;
+  const long long wq = (long long)D.Hq * D.d, wk = (long long)D.Hkv * D.d;
+  if (q && (!rows_ok(D, q, q_row, wq) || !rows_ok(D, q_out, q_out_row, wq) || (q == q_out && q_row != q_out_row)))
+    return QSA_ERR_INVALID_ARG;
+  if (k && (!rows_ok(D, k, k_row, wk) || !rows_ok(D, k_out, k_out_row, wk) || (k == k_out && k_row != k_out_row)))
+    return QSA_ERR_INVALID_ARG;
+  AppendArgs A = {};
+  A.q = q;
+  A.q_row = q_row;
+  A.q_out = q_out;
+  A.q_out_row = q_out_row;
+  A.k = k;
+  A.k_row = k_row;
+  A.k_out = k_out;
+  A.k_out_row = k_out_row;
+  return cuda_status(launch_norm_rope(D, N, pos, n_tok, A, (cudaStream_t)stream));
+}
+
+qsa_status_t qsa_paged_append(const qsa_config_t *cfg, const qsa_norm_rope_t *nr, const qsa_paged_t *pg,
+                              const qsa_append_t *t, void *workspace, size_t workspace_bytes, qsa_stream_t stream) {
+  g_serial_at_entry = g_error_serial;
+  Dims D;
+  NormRope N;
+  Paged G;
+  qsa_status_t s = resolve(cfg, &D);
+  if (s != QSA_OK) return s;
+  if (!t) return QSA_ERR_INVALID_ARG;
+  if ((s = resolve_norm_rope(D, nr, &N)) != QSA_OK) return s;
+  if ((s = resolve_paged(pg, &G)) != QSA_OK) return s;
+  if (G.batch == 0 || G.n_tok == 0) return QSA_OK;
+  if (!G.q_start || !G.kv_len || !G.table || !t->k_pages || !t->v_pages || !aligned16(t->k_pages) ||
+      !aligned16(t->v_pages) || !workspace || !aligned16(workspace) || workspace_bytes < kStatusBytes)
+    return QSA_ERR_INVALID_ARG;
+  const long long wq = (long long)D.Hq * D.d, wk = (long long)D.Hkv * D.d;
+  if (!rows_ok(D, t->k, t->k_row, wk) || !rows_ok(D, t->v, t->v_row, wk)) return QSA_ERR_INVALID_ARG;
+  if (t->q && (!rows_ok(D, t->q, t->q_row, wq) || !rows_ok(D, t->q_out, t->q_out_row, wq) ||
+               (t->q == t->q_out && t->q_row != t->q_out_row)))
+    return QSA_ERR_INVALID_ARG;
+  if (t->ki && (!rows_ok(D, t->ki, t->ki_row, D.di) || !t->ki_cache || !aligned16(t->ki_cache) || t->ki_cap < 0))
+    return QSA_ERR_INVALID_ARG;
+  AppendArgs A = {};
+  A.q = t->q;
+  A.k = t->k;
+  A.v = t->v;
+  A.ki = t->ki;
+  A.q_row = t->q_row;
+  A.k_row = t->k_row;
+  A.v_row = t->v_row;
+  A.ki_row = t->ki_row;
+  A.q_out = t->q_out;
+  A.q_out_row = t->q_out_row;
+  A.k_pages = t->k_pages;
+  A.v_pages = t->v_pages;
+  A.ki_cache = t->ki_cache;
+  A.ki_cap = t->ki_cap;
+  return cuda_status(launch_paged_append(D, N, G, A, status_word(workspace), (cudaStream_t)stream));
+}
+
+qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t *pg, size_t *bytes) {
+  Dims D;
+  Paged G;
+  qsa_status_t s = resolve(cfg, &D);
+  if (s != QSA_OK) return s;
+  if (!bytes) return QSA_ERR_INVALID_ARG;
+  if ((s = resolve_paged(pg, &G)) != QSA_OK) return s;
+  *bytes = kStatusBytes + round256(paged_rows_workspace(D));
+  return QSA_OK;
+}
+
+qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, const void *q, const void *k_pages,
+                            const void *v_pages, const int32_t *sel, void *out, void *workspace,
+                            size_t workspace_bytes, qsa_stream_t stream) {
+  g_serial_at_entry = g_error_serial;
+  Dims D;
+  Paged G;
+  qsa_status_t s = resolve(cfg, &D);
+  if (s != QSA_OK) return s;
+  if ((s = resolve_paged(pg, &G)) != QSA_OK) return s;
+  if (G.batch == 0 || G.n_tok == 0) return QSA_OK;
+  if (!G.q_start || !G.kv_len || !G.table || !q || !k_pages || !v_pages || !out || !workspace)
+    return QSA_ERR_INVALID_ARG;
+  const void *ptrs[] = {q, k_pages, v_pages, sel, out, workspace};
+  for (const void *p : ptrs)
+    if (!aligned16(p)) return QSA_ERR_INVALID_ARG;
+  if (workspace_bytes < kStatusBytes + paged_rows_workspace(D)) return QSA_ERR_INVALID_ARG;
+  return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, (char *)workspace + kStatusBytes,
+                                       status_word(workspace), (cudaStream_t)stream));
+}
+
 qsa_status_t qsa_read_device_status(void *workspace, qsa_stream_t stream, qsa_status_t *status) {
   if (!workspace || !status) return QSA_ERR_INVALID_ARG;
   int h = 0;

@@ -203,4 +203,59 @@ cudaError_t launch_offload_gather(const Dims &D, const Seqs &S, const void *k_ca
                                   const void *k_new, const void *v_new, const int32_t *sel, void *k_stage,
                                   void *v_stage, int32_t *sel_stage, int32_t *len_stage, cudaStream_t st);
 
+// ---- paged cache (qsa_paged_t) ----
+
+// Geometry of a packed batch over a paged cache (device pointers).
+struct Paged {
+  const int32_t *q_start, *kv_len, *table;
+  int batch, n_tok, max_chunk;
+  int ps, ps_shift;  // tokens per page, a power of two
+  int n_pages, max_pages;
+};
+
+// One sequence of the batch: first packed row, new tokens, tokens in the cache.
+struct PagedSeq {
+  int q0, n, len;
+  bool ok;
+};
+
+// True geometry, or ok = false (and the device check recorded) when it does not fit.
+__device__ __forceinline__ PagedSeq paged_seq(const Paged &P, int b, int *status) {
+  PagedSeq s;
+  const int q0 = P.q_start[b], q1 = P.q_start[b + 1], len = P.kv_len[b];
+  s.ok = q0 >= 0 && q1 >= q0 && q1 <= P.n_tok && q1 - q0 <= P.max_chunk && len >= q1 - q0 &&
+         (long long)len <= ((long long)P.max_pages << P.ps_shift);
+  if (!s.ok) record_status(status, QSA_ERR_DEVICE_CHECK);
+  s.q0 = q0;
+  s.n = s.ok ? q1 - q0 : 0;
+  s.len = s.ok ? len : 0;
+  return s;
+}
+
+// Norm + rotation of head rows (qsa_norm_rope) and the append (qsa_paged_append). A null
+// pos takes each row's position from the paged batch.
+struct NormRope {
+  float eps, w_off;
+  double log2_theta;
+  int rot, rot_i;
+  const void *qw, *kw;
+};
+struct AppendArgs {
+  const void *q, *k, *v, *ki;
+  long long q_row, k_row, v_row, ki_row, q_out_row, k_out_row;
+  void *q_out, *k_out;               // k_out: the dense output of qsa_norm_rope
+  void *k_pages, *v_pages, *ki_cache;
+  int ki_cap;
+};
+cudaError_t launch_norm_rope(const Dims &D, const NormRope &N, const int32_t *pos, int n_tok, const AppendArgs &A,
+                             cudaStream_t st);
+cudaError_t launch_paged_append(const Dims &D, const NormRope &N, const Paged &P, const AppendArgs &A, int *status,
+                                cudaStream_t st);
+
+// Attention over the paged cache, few (token, head) rows per sequence or shapes that the
+// tensor-core chunk kernels do not serve; sel null: every visible token.
+size_t paged_rows_workspace(const Dims &D);
+cudaError_t launch_paged_rows(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *sel, void *out, void *scratch, int *status, cudaStream_t st);
+
 }  // namespace qsa

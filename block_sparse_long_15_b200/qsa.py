@@ -54,12 +54,32 @@ class qsa_tensors_t(ctypes.Structure):
                 ("sel", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+class qsa_paged_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_tok", ctypes.c_int32), ("max_chunk", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class qsa_norm_rope_t(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("rope_theta", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("indexer_rotary_dim", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class qsa_append_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_row", ctypes.c_int64), ("q_out", ctypes.c_void_p), ("q_out_row", ctypes.c_int64),
+                ("ki", ctypes.c_void_p), ("ki_row", ctypes.c_int64), ("ki_cache", ctypes.c_void_p),
+                ("ki_cap", ctypes.c_int32)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"QSA CUDA library not built: {LIB_PATH} is missing "
                           "(run block_sparse_long_15_b200.build.build())")
     L = ctypes.CDLL(LIB_PATH)
-    P, V, I, S = ctypes.POINTER, ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, V, I, S, L64 = ctypes.POINTER, ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
     cfgp = P(qsa_config_t)
     sig = {
         "qsa_config_validate": ([cfgp], I),
@@ -82,6 +102,10 @@ def _load() -> ctypes.CDLL:
         "qsa_selftest_wait_timeout": ([V, ctypes.c_int64, V], I),
         "qsa_offload_staging_size": ([cfgp, I, P(S)], I),
         "qsa_decode_offload": ([cfgp, P(qsa_tensors_t), V, S, V, S, V], I),
+        "qsa_norm_rope": ([cfgp, P(qsa_norm_rope_t), V, I, V, L64, V, L64, V, L64, V, L64, V], I),
+        "qsa_paged_append": ([cfgp, P(qsa_norm_rope_t), P(qsa_paged_t), P(qsa_append_t), V, S, V], I),
+        "qsa_paged_workspace_size": ([cfgp, P(qsa_paged_t), P(S)], I),
+        "qsa_paged_attn": ([cfgp, P(qsa_paged_t), V, V, V, V, V, V, S, V], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -96,7 +120,8 @@ EXPORTED = ("qsa_config_validate", "qsa_topk_blocks", "qsa_status_string", "qsa_
             "qsa_read_device_status", "qsa_abi_version", "qsa_attn_kernel_name",
             "qsa_kernel_launch_count", "qsa_last_error", "qsa_sparse_attn_decode_noalloc",
             "qsa_selftest_wait_timeout", "qsa_offload_staging_size", "qsa_decode_offload",
-            "qsa_index_scores", "qsa_select_topk", "qsa_project")
+            "qsa_index_scores", "qsa_select_topk", "qsa_project", "qsa_norm_rope", "qsa_paged_append",
+            "qsa_paged_workspace_size", "qsa_paged_attn")
 
 # Size of the library's fixed decode scratch (QSA_NOALLOC_SCRATCH_BYTES in qsa.h).
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -366,6 +391,147 @@ def qsa_decode_offload(cfg, t: Dict[str, torch.Tensor], staging, workspace, stre
                       _p(t["kv_start"]), _p(t["kv_len"]), None, _p(t["sel"]), _p(t["out"]))
     _check(_lib.qsa_decode_offload(ctypes.byref(cfg), ctypes.byref(T), _p(staging), staging.numel(),
                                    _p(workspace), workspace.numel(), _stream(stream)), "qsa_decode_offload")
+
+
+# --------------------------------------------------------------------------- paged cache
+class NormRope:
+    """Norm and rotation parameters (qsa_norm_rope_t) with the weights they point to."""
+
+    def __init__(self, q_weight, k_weight, eps: float, weight_offset: float, rope_theta: float, rotary_dim: int,
+                 indexer_rotary_dim: int):
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.c = qsa_norm_rope_t(eps, weight_offset, rope_theta, rotary_dim, indexer_rotary_dim, _p(q_weight),
+                                 _p(k_weight))
+
+
+def make_norm_rope(q_weight=None, k_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
+                   rope_theta: float = 1e4, rotary_dim: int = 0, indexer_rotary_dim: int = 0) -> NormRope:
+    """q_weight / k_weight: [head_dim] of the config's dtype; None leaves that side without the norm.
+    weight_offset=1.0 for weights stored around zero; rotary_dim=0 for no rotation."""
+    return NormRope(q_weight, k_weight, eps, weight_offset, rope_theta, rotary_dim, indexer_rotary_dim)
+
+
+class PagedBatch:
+    """A packed batch over a paged cache (qsa_paged_t) with the device tensors it points to."""
+
+    def __init__(self, q_start, kv_len, page_table, n_tok: int, max_chunk: int, page_size: int, n_pages: int):
+        batch = kv_len.shape[0]
+        _want_lengths(batch, kv_len=kv_len)
+        _want(q_start, torch.int32, (batch + 1,), "q_start")
+        _want(page_table, torch.int32, (batch, page_table.shape[1]), "page_table")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.n_tok, self.page_size, self.n_pages = n_tok, page_size, n_pages
+        self.c = qsa_paged_t(batch, n_tok, max_chunk, page_size, n_pages, page_table.shape[1], _p(q_start), _p(kv_len),
+                             _p(page_table))
+
+
+def make_paged(q_start, kv_len, page_table, *, n_tok: int, max_chunk: int, page_size: int, n_pages: int) -> PagedBatch:
+    """q_start [batch + 1], kv_len [batch], page_table [batch][max_pages], all int32. The tensors may be
+    refilled between calls (they are read on the device); n_tok rows are packed, and no sequence has more
+    than max_chunk of them."""
+    return PagedBatch(q_start, kv_len, page_table, n_tok, max_chunk, page_size, n_pages)
+
+
+def qsa_paged_workspace_size(cfg, pg: PagedBatch) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.qsa_paged_workspace_size(ctypes.byref(cfg), ctypes.byref(pg.c), ctypes.byref(out)),
+           "qsa_paged_workspace_size")
+    return out.value
+
+
+def alloc_paged_workspace(cfg, pg: PagedBatch, device=None) -> torch.Tensor:
+    """Zeroed workspace bytes for qsa_paged_attn (and qsa_paged_append)."""
+    return torch.zeros(qsa_paged_workspace_size(cfg, pg), dtype=torch.uint8, device=device or pg.kv_len.device)
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape, name: str):
+    """(address, row stride) of packed rows: everything behind the first axis is dense."""
+    _want(t, dtype, shape, name)
+    if not t.is_cuda:
+        raise ValueError("QSA tensors must live on a CUDA device")
+    want = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if st != want and n != 1:
+            raise ValueError(f"{name}: a row's heads must be dense")
+        want *= n
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), want)
+
+
+def _same_device(first: torch.Tensor, *others):
+    """The call runs on the current device: every tensor has to be there."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def qsa_norm_rope(cfg, nr: NormRope, pos, q, k, q_out, k_out, stream=None):
+    """RMS norm and rotation of q [n][Hq][d] and k [n][Hkv][d] (rows may be strided) at pos [n] into
+    q_out / k_out, which may be q / k themselves. q and q_out, or k and k_out, may be None."""
+    dt, n = _elem(cfg), pos.shape[0]
+    _want(pos, torch.int32, (n,), "pos")
+    a = [None, 0, None, 0, None, 0, None, 0]
+    if q is not None:
+        shape = (n, cfg.num_attention_heads, cfg.head_dim)
+        a[0:2], a[2:4] = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
+    if k is not None:
+        shape = (n, cfg.num_key_value_heads, cfg.head_dim)
+        a[4:6], a[6:8] = _rows(k, dt, shape, "k"), _rows(k_out, dt, shape, "k_out")
+    _norm_weights(cfg, nr)
+    _same_device(pos, q, k, q_out, k_out, nr.q_weight, nr.k_weight)
+    _check(_lib.qsa_norm_rope(ctypes.byref(cfg), ctypes.byref(nr.c), _p(pos), n, *a, _stream(stream)), "qsa_norm_rope")
+
+
+def _norm_weights(cfg, nr: NormRope):
+    for name, w in (("q_weight", nr.q_weight), ("k_weight", nr.k_weight)):
+        if w is not None:
+            _want(w, _elem(cfg), (cfg.head_dim,), name)
+
+
+def qsa_paged_append(cfg, nr: Optional[NormRope], pg: PagedBatch, k, v, k_pages, v_pages, workspace, q=None, q_out=None,
+                     ki=None, ki_cache=None, stream=None):
+    """Appends the packed rows k, v [n_tok][Hkv][d] to the pages, k normed and rotated on the way (nr), with
+    q [n_tok][Hq][d] into q_out and ki [n_tok][di] into ki_cache [batch][cap][di] beside them."""
+    dt, n, Hkv, d = _elem(cfg), pg.n_tok, cfg.num_key_value_heads, cfg.head_dim
+    pool = (pg.n_pages, Hkv, pg.page_size, d)
+    _want(k_pages, dt, pool, "k_pages")
+    _want(v_pages, dt, pool, "v_pages")
+    t = qsa_append_t()
+    t.k, t.k_row = _rows(k, dt, (n, Hkv, d), "k")
+    t.v, t.v_row = _rows(v, dt, (n, Hkv, d), "v")
+    t.k_pages, t.v_pages = _p(k_pages), _p(v_pages)
+    if q is not None:
+        shape = (n, cfg.num_attention_heads, d)
+        t.q, t.q_row = _rows(q, dt, shape, "q")
+        t.q_out, t.q_out_row = _rows(q_out, dt, shape, "q_out")
+    if ki is not None:
+        t.ki, t.ki_row = _rows(ki, dt, (n, cfg.indexer_head_dim), "ki")
+        _want(ki_cache, dt, (pg.c.batch, ki_cache.shape[1], cfg.indexer_head_dim), "ki_cache")
+        t.ki_cache, t.ki_cap = _p(ki_cache), ki_cache.shape[1]
+    if nr is not None:
+        _norm_weights(cfg, nr)
+        _same_device(k, nr.q_weight, nr.k_weight)
+    _same_device(k, v, k_pages, v_pages, workspace, q, q_out, ki, ki_cache, pg.q_start, pg.kv_len, pg.page_table)
+    _check(_lib.qsa_paged_append(ctypes.byref(cfg), ctypes.byref(nr.c) if nr is not None else None, ctypes.byref(pg.c),
+                                 ctypes.byref(t), _p(workspace), workspace.numel(), _stream(stream)), "qsa_paged_append")
+
+
+def qsa_paged_attn(cfg, pg: PagedBatch, q, k_pages, v_pages, sel, out, workspace, stream=None):
+    """Attention of the packed rows q [n_tok][Hq][d] over the pages [n_pages][Hkv][page_size][d], over every
+    visible token (sel None) or the blocks in sel [n_tok][k] and the trailing range."""
+    dt, n, d = _elem(cfg), pg.n_tok, cfg.head_dim
+    pool = (pg.n_pages, cfg.num_key_value_heads, pg.page_size, d)
+    _want(q, dt, (n, cfg.num_attention_heads, d), "q")
+    _want(out, dt, (n, cfg.num_attention_heads, d), "out")
+    _want(k_pages, dt, pool, "k_pages")
+    _want(v_pages, dt, pool, "v_pages")
+    if sel is not None:
+        _want(sel, torch.int32, (n, qsa_topk_blocks(cfg)), "sel")
+    _same_device(q, k_pages, v_pages, sel, out, workspace, pg.q_start, pg.kv_len, pg.page_table)
+    _check(_lib.qsa_paged_attn(ctypes.byref(cfg), ctypes.byref(pg.c), _p(q), _p(k_pages), _p(v_pages), _p(sel), _p(out),
+                               _p(workspace), workspace.numel(), _stream(stream)), "qsa_paged_attn")
 
 
 def qsa_selftest_wait_timeout(workspace, limit_ns: int = 50_000_000, stream=None):

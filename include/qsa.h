@@ -25,8 +25,8 @@
  *
  * Conventions shared by every entry point
  * ---------------------------------------
- * Memory. Every pointer argument except `cfg`, `t` and `bytes` is a DEVICE
- * pointer owned by the caller; the library never allocates, frees or keeps a
+ * Memory. Every pointer argument except `cfg`, `t`, `pc`, `nr`, `pg`, `status` and
+ * `bytes` is a DEVICE pointer owned by the caller; the library never allocates, frees or keeps a
  * pointer past the call, and only qsa_read_device_status synchronises. All work
  * is enqueued on `stream` (a cudaStream_t; NULL = the legacy default stream),
  * so results are ready when the stream is. Base pointers must be 16-byte
@@ -320,6 +320,114 @@ qsa_status_t qsa_offload_staging_size(const qsa_config_t *cfg, int32_t batch, si
 qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t, void *staging,
                                 size_t staging_bytes, void *workspace, size_t workspace_bytes,
                                 qsa_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Serving from a paged cache. A serving process holds the K/V cache in pages that
+ * its sequences share out among themselves, and runs a batch of sequences with a
+ * few new tokens each: one for a decode step, some for drafted tokens, many for a
+ * chunk of a prompt. A step is qsa_project (rotary_dim 0 leaves q and k unrotated),
+ * qsa_paged_append, then, on a layer with QSA, qsa_compress_blocks and
+ * qsa_index_score_topk on the indexer's own cache (which stays one plane per
+ * sequence), and qsa_paged_attn over the pages. (The model page has paged caches
+ * nowhere; the layouts here are this library's.)
+ *
+ * The batch is packed: the new tokens of sequence b are rows q_start[b] ..
+ * q_start[b + 1] - 1 of every packed tensor, and with n = q_start[b + 1] -
+ * q_start[b], row q_start[b] + i sits at position t = kv_len[b] - n + i. A sequence
+ * may have no new token. Rows before q_start[0] and from q_start[batch] on belong to
+ * no sequence: they are not read and nothing is written for them.
+ *
+ * Pages: k_pages, v_pages [n_pages][Hkv][page_size][d]. Token u of sequence b sits in
+ * slot u % page_size of page page_table[b][u / page_size]; entries behind a
+ * sequence's last page are not read. Sequences may share pages that no call writes.
+ * Slots behind a sequence's last token may hold anything, NaN included. Inside a
+ * sequence keys and values are finite: a NaN or infinity in a value row may reach the
+ * earlier tokens of the same chunk, though not another sequence.
+ *
+ * A sequence whose geometry does not fit (q_start that falls or passes n_tok, more
+ * new tokens than max_chunk or kv_len, kv_len beyond max_pages * page_size) or that
+ * needs a page outside [0, n_pages) records QSA_ERR_DEVICE_CHECK in the workspace
+ * status word; nothing out of range is read or written for it, its own rows and
+ * slots are unspecified, and the other sequences are served. */
+typedef struct {
+  int32_t batch;             /* sequences */
+  int32_t n_tok;             /* rows of the packed tensors */
+  int32_t max_chunk;         /* no sequence has more new tokens than this; kernels are picked by it */
+  int32_t page_size;         /* tokens a page holds: a power of two, 16 .. 32768 */
+  int32_t n_pages;           /* pages of the pool */
+  int32_t max_pages;         /* entries of a row of page_table */
+  const int32_t *q_start;    /* [batch + 1] */
+  const int32_t *kv_len;     /* [batch] tokens of the sequence, the new ones included */
+  const int32_t *page_table; /* [batch][max_pages] */
+} qsa_paged_t;
+
+/* RMS norm of each head over its d elements and rotary position embedding:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset), then
+ *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a), j = i + rotary_dim / 2,
+ *   i < rotary_dim / 2, a = position * rope_theta^(-2i / rotary_dim)
+ * in fp32, with the angle taken modulo a turn in 64-bit integers, and rounded to
+ * cfg->dtype once. weight_offset is 1 for weights stored around zero. */
+typedef struct {
+  float eps;                  /* >= 0 */
+  float weight_offset;
+  float rope_theta;           /* > 0 where something rotates */
+  int32_t rotary_dim;         /* multiple of 16, <= head_dim; 0: q and k do not rotate */
+  int32_t indexer_rotary_dim; /* multiple of 16, <= indexer_head_dim; 0: ki does not rotate */
+  const void *q_weight;       /* [d] of cfg->dtype, device memory; NULL: queries are not normed */
+  const void *k_weight;       /* [d]; NULL: keys are not normed */
+} qsa_norm_rope_t;
+
+/* Norm and rotation of the query heads q [n_tok][Hq][d] and key heads k [n_tok][Hkv][d]
+ * in one pass, row r at position pos[r] (any int32). A row's heads are dense; rows are
+ * *_row elements apart (a multiple of 16 bytes), so that q and k may be read out of the
+ * rows of a fused projection. q_out / k_out may be q / k (with the same row stride) but
+ * must not overlap them otherwise. q or k may be NULL, with its output: the other one
+ * alone is done. No workspace. For indexer heads, call it with a config whose
+ * head_dim is the indexer's. */
+qsa_status_t qsa_norm_rope(const qsa_config_t *cfg, const qsa_norm_rope_t *nr, const int32_t *pos, int32_t n_tok,
+                           const void *q, int64_t q_row, void *q_out, int64_t q_out_row, const void *k, int64_t k_row,
+                           void *k_out, int64_t k_out_row, qsa_stream_t stream);
+
+/* What qsa_paged_append reads and writes. */
+typedef struct {
+  const void *k, *v;           /* [n_tok][Hkv][d] packed rows, k_row / v_row elements apart */
+  int64_t k_row, v_row;
+  void *k_pages, *v_pages;
+  const void *q;               /* [n_tok][Hq][d], or NULL */
+  int64_t q_row;
+  void *q_out;                 /* [n_tok][Hq][d], rows q_out_row elements apart */
+  int64_t q_out_row;
+  const void *ki;              /* [n_tok][di], or NULL */
+  int64_t ki_row;
+  void *ki_cache;              /* [batch][ki_cap][di]: qsa_tensors_t's, with kv_start = 0 */
+  int32_t ki_cap;
+} qsa_append_t;
+
+/* Appends the batch's new tokens to the paged cache: k, normed and rotated at its
+ * position on the way, and v as it is, into their slots; with q set, the queries are
+ * normed and rotated in the same pass into q_out; with ki set, the indexer keys are
+ * rotated (indexer_rotary_dim) into ki_cache[b][t]. nr NULL: everything is copied as it
+ * is. A sequence longer than ki_cap records QSA_ERR_DEVICE_CHECK and its ki is not
+ * written. q_out may be q (same stride). No two sequences may append to one slot.
+ * workspace: at least the 256-byte status word. */
+qsa_status_t qsa_paged_append(const qsa_config_t *cfg, const qsa_norm_rope_t *nr, const qsa_paged_t *pg,
+                              const qsa_append_t *t, void *workspace, size_t workspace_bytes, qsa_stream_t stream);
+
+/* Bytes of workspace that qsa_paged_attn needs for this batch (the pointers of pg are
+ * not read); the rules of qsa_workspace_size hold for it. */
+qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t *pg, size_t *bytes);
+
+/* Attention of the batch's new tokens over the paged cache, their own keys and values
+ * included: q, out [n_tok][Hq][d] (dense). With sel NULL a row at position t attends
+ * every token u <= t (a full-attention layer without the indexer). With sel [n_tok][k],
+ * as qsa_index_score_topk writes it for the rows, it attends the listed blocks below
+ * n_c(t) and its trailing range [n_c B, t], as in qsa_sparse_attn; a row that sees no
+ * token is written as zeros. Accumulation is fp32; outputs are rounded once at the end.
+ * The result does not depend on the batch's order of execution: equal calls give equal
+ * bits. */
+qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, const void *q, const void *k_pages,
+                            const void *v_pages, const int32_t *sel, void *out, void *workspace,
+                            size_t workspace_bytes, qsa_stream_t stream);
 
 #ifdef __cplusplus
 }

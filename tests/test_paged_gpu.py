@@ -1,0 +1,218 @@
+"""The paged-cache operators through the binding, against plain 64-bit forms (paged_util)."""
+import math
+
+import pytest
+import torch
+
+from tests import paged_util as U
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+NAN = float("nan")
+
+
+def _cfg(qsa, Hq=16, Hkv=2, d=128, di=64, block=64, topk=4, dtype="bf16", scale=0.0):
+    return qsa.make_config(Hq, Hkv, d, 4, di, block, topk, dtype, scale)
+
+
+# ------------------------------------------------------------------ norm + rotation
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,rot,w_off,pad", [
+    ("bf16", 16, 2, 128, 128, 0.0, 0),
+    ("bf16", 32, 4, 128, 64, 1.0, 264),    # rows of a fused projection
+    ("bf16", 4, 1, 64, 32, 0.0, 8),
+    ("bf16", 16, 2, 256, 256, 0.0, 0),
+    ("bf16", 3, 3, 80, 80, 0.0, 0),        # a head that does not fill its lanes
+    ("bf16", 33, 11, 8, 0, 0.0, 0),        # one lane a head, no rotation
+    ("fp32", 4, 1, 64, 64, 0.0, 0),
+    ("fp32", 5, 5, 96, 16, 1.0, 4),
+    ("fp32", 2, 1, 256, 128, 0.0, 0),
+])
+@pytest.mark.parametrize("n", [1, 37])
+def test_norm_rope(cuda_lib, dtype, Hq, Hkv, d, rot, w_off, pad, n):
+    qsa, dt = cuda_lib, DT[dtype]
+    g = torch.Generator().manual_seed(d + rot + n)
+    q = torch.randn(n, Hq * d + pad, generator=g).to(dt).cuda()[:, : Hq * d].unflatten(1, (Hq, d))
+    k = (3 * torch.randn(n, Hkv * d + pad, generator=g)).to(dt).cuda()[:, : Hkv * d].unflatten(1, (Hkv, d))
+    qw, kw = ((torch.randn(d, generator=g) * 0.3 + 1 - w_off).to(dt).cuda() for _ in range(2))
+    pos = torch.randint(0, 200000, (n,), generator=g).to(torch.int32)
+    pos[:1] = 2 ** 31 - 1 if n == 1 else 0
+    if n > 3:
+        pos[1], pos[2] = -5, 2 ** 31 - 1
+    pos = pos.cuda()
+    nr = qsa.make_norm_rope(qw, kw, eps=1e-5, weight_offset=w_off, rope_theta=1e6, rotary_dim=rot)
+    qo, ko = torch.full((n, Hq, d), NAN, dtype=dt, device="cuda"), torch.full((n, Hkv, d), NAN, dtype=dt, device="cuda")
+    q0, k0 = q.clone(), k.clone()
+    qsa.qsa_norm_rope(_cfg(qsa, Hq, Hkv, d, dtype=dtype), nr, pos, q, k, qo, ko)
+    for name, x, x0, w, out in (("q", q, q0, qw, qo), ("k", k, k0, kw, ko)):
+        want, tol = U.norm_rope(x0, w, pos, 1e-5, w_off, rot, 1e6)
+        U.check(out, want, tol, name)
+        assert torch.equal(x, x0)
+    # in place, and one side alone: the same bits
+    qsa.qsa_norm_rope(_cfg(qsa, Hq, Hkv, d, dtype=dtype), nr, pos, q, None, q, None)
+    qsa.qsa_norm_rope(_cfg(qsa, Hq, Hkv, d, dtype=dtype), nr, pos, None, k, None, k)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
+def test_norm_rope_without_weight_only_rotates(cuda_lib):
+    qsa = cuda_lib
+    q = torch.randn(5, 4, 64).cuda()
+    pos = torch.tensor([0, 1, 2, 70000, 9], dtype=torch.int32).cuda()
+    out = torch.empty_like(q)
+    nr = qsa.make_norm_rope(rope_theta=1e4, rotary_dim=32)
+    qsa.qsa_norm_rope(_cfg(qsa, 4, 1, 64, dtype="fp32"), nr, pos, q, None, out, None)
+    U.check(out, *U.norm_rope(q, None, pos, 0.0, 0.0, 32, 1e4), "q")
+    assert torch.equal(out[..., 32:], q[..., 32:]) and torch.equal(out[0], q[0])
+
+
+def test_norm_rope_extreme_rows(cuda_lib):
+    """Rows of zeros stay zeros; the largest and smallest magnitudes of bf16 inputs stay finite where
+    the mean of squares does in fp32."""
+    qsa = cuda_lib
+    q = torch.zeros(3, 2, 128)
+    q[1] = 1e15
+    q[2] = 1e-15
+    q = q.to(torch.bfloat16).cuda()
+    w = torch.ones(128, dtype=torch.bfloat16).cuda()
+    out = torch.empty_like(q)
+    pos = torch.tensor([3, 4, 5], dtype=torch.int32).cuda()
+    nr = qsa.make_norm_rope(w, w, eps=1e-6, rope_theta=1e4, rotary_dim=128)
+    qsa.qsa_norm_rope(_cfg(qsa, 2, 1, 128), nr, pos, q, None, out, None)
+    assert (out[0] == 0).all()
+    U.check(out, *U.norm_rope(q, w, pos, 1e-6, 0.0, 128, 1e4), "q")
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,page,q_len,kv_len,rot,rot_i", [
+    ("bf16", 16, 2, 128, 64, [1] * 5, [1, 64, 65, 200, 128], 128, 64),
+    ("bf16", 32, 4, 128, 16, [0, 37, 1, 16, 0], [5, 37, 16, 100, 1], 64, 32),
+    ("fp32", 4, 1, 64, 32, [3, 0, 40], [33, 1, 40], 64, 0),
+    ("bf16", 16, 2, 256, 256, [70], [300], 256, 64),
+    ("bf16", 3, 3, 80, 16, [5, 6], [21, 6], 16, 16),
+])
+def test_append(cuda_lib, dtype, Hq, Hkv, d, page, q_len, kv_len, rot, rot_i):
+    qsa, dt, di = cuda_lib, DT[dtype], 64
+    g = U.make_batch(q_len, kv_len, page, seed=7, lead=2, tail=3)
+    gen = torch.Generator().manual_seed(3)
+    n = g["n_tok"]
+    rows = {}
+    for name, heads, width in (("q", Hq, d), ("k", Hkv, d), ("v", Hkv, d), ("ki", 1, di)):
+        x = torch.randn(n, heads, width, generator=gen)
+        x[:2] = NAN
+        x[n - 3:] = NAN  # rows of no sequence
+        rows[name] = x.to(dt).cuda()
+    qw, kw = ((torch.randn(d, generator=gen) * 0.3 + 1).to(dt).cuda() for _ in range(2))
+    cap = max(kv_len) + 3
+    kp, vp = U.pools(Hkv, d, g, kv_len, dt, seed=1)
+    ki_cache = torch.randn(len(q_len), cap, di, generator=gen).to(dt).cuda()
+    q_out = torch.full((n, Hq, d), 7.0, dtype=dt, device="cuda")
+    want_k, want_v, want_ki = kp.clone(), vp.clone(), ki_cache.clone()
+    pg = qsa.make_paged(**g)
+    nr = qsa.make_norm_rope(qw, kw, eps=1e-6, rope_theta=1e6, rotary_dim=rot, indexer_rotary_dim=rot_i)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qsa.qsa_paged_append(_cfg(qsa, Hq, Hkv, d, di, dtype=dtype), nr, pg, rows["k"], rows["v"], kp, vp, ws, q=rows["q"],
+                         q_out=q_out, ki=rows["ki"][:, 0], ki_cache=ki_cache)
+    assert qsa.qsa_read_device_status(ws) == qsa.QSA_OK
+    where = [(r + 2, b, t) for r, b, t in U.positions(q_len, kv_len)]
+    r = torch.tensor([x[0] for x in where]).cuda()
+    b = torch.tensor([x[1] for x in where]).cuda()
+    t = torch.tensor([x[2] for x in where]).cuda()
+    pages = g["page_table"][b, t // page].long()
+    U.check(q_out[r], *U.norm_rope(rows["q"][r], qw, t, 1e-6, 0.0, rot, 1e6), "q")
+    U.check(kp[pages, :, t % page], *U.norm_rope(rows["k"][r], kw, t, 1e-6, 0.0, rot, 1e6), "k")
+    U.check(ki_cache[b, t][:, None], *U.norm_rope(rows["ki"][r], None, t, 0.0, 0.0, rot_i, 1e6), "ki")
+    assert torch.equal(vp[pages, :, t % page], rows["v"][r])
+    # nothing else moved: slots, cache rows, and the packed rows of no sequence
+    for got, want, at in ((kp, want_k, (pages, slice(None), t % page)), (vp, want_v, (pages, slice(None), t % page)),
+                          (ki_cache, want_ki, (b, t))):
+        want[at] = got[at]
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    assert (q_out[:2] == 7).all() and (q_out[n - 3:] == 7).all()
+
+
+def test_append_copies_without_norm_rope(cuda_lib):
+    qsa = cuda_lib
+    g = U.make_batch([4, 1], [20, 17], 16, seed=1)
+    k, v = (torch.randn(5, 2, 128).to(torch.bfloat16).cuda() for _ in range(2))
+    kp, vp = (torch.zeros(g["n_pages"], 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qsa.qsa_paged_append(_cfg(qsa), None, qsa.make_paged(**g), k, v, kp, vp, ws)
+    for r, b, t in U.positions([4, 1], [20, 17]):
+        p = int(g["page_table"][b, t // 16])
+        assert torch.equal(kp[p, :, t % 16], k[r]) and torch.equal(vp[p, :, t % 16], v[r])
+
+
+# ------------------------------------------------------------------ attention
+CASES = [
+    # dtype Hq Hkv d page block topk q_len kv_len
+    ("bf16", 16, 2, 128, 64, 64, 0, [1] * 4, [1, 63, 64, 1000]),
+    ("bf16", 16, 2, 128, 16, 64, 0, [1, 0, 1], [17, 40, 16]),
+    ("bf16", 16, 2, 128, 64, 64, 4, [1] * 5, [1, 63, 64, 1000, 333]),
+    ("bf16", 16, 2, 128, 32, 32, 3, [2, 0, 5], [70, 9, 500]),
+    ("bf16", 16, 2, 256, 64, 64, 0, [3, 4, 1], [300, 4, 129]),
+    ("bf16", 16, 2, 256, 16, 64, 2, [4, 1], [300, 129]),
+    ("bf16", 8, 8, 128, 128, 64, 0, [1, 7, 30], [140, 7, 300]),
+    ("bf16", 24, 8, 64, 256, 64, 0, [1, 6, 40], [700, 6, 300]),
+    ("bf16", 24, 8, 64, 16, 32, 5, [6, 40], [6, 300]),
+    ("bf16", 16, 1, 128, 64, 128, 2, [1, 9], [700, 400]),
+    ("bf16", 32, 1, 64, 32, 64, 2, [1, 3], [200, 400]),
+    ("bf16", 6, 2, 80, 16, 64, 0, [2, 20], [50, 200]),
+    ("bf16", 6, 2, 128, 16, 24, 3, [2, 20], [50, 200]),
+    ("bf16", 16, 2, 128, 64, 64, 0, [70, 1, 129], [500, 300, 129]),
+    ("bf16", 16, 2, 128, 16, 64, 4, [70, 1, 129], [500, 300, 129]),
+    ("bf16", 16, 2, 256, 64, 64, 0, [70, 1, 129], [500, 300, 129]),
+    ("bf16", 16, 2, 256, 16, 64, 4, [70, 1, 129], [500, 300, 129]),
+    ("bf16", 24, 8, 128, 32, 64, 0, [150, 3, 0, 44], [150, 300, 10, 600]),
+    ("bf16", 24, 8, 128, 32, 64, 3, [150, 3, 0, 44], [150, 300, 10, 600]),
+    ("bf16", 4, 4, 128, 256, 128, 2, [200, 20], [600, 20]),
+    ("fp32", 4, 1, 64, 16, 32, 4, [30, 1, 0, 7], [200, 300, 4, 7]),
+    ("fp32", 4, 1, 64, 16, 32, 0, [30, 1, 0, 7], [200, 300, 4, 7]),
+    ("fp32", 8, 2, 256, 64, 48, 2, [1, 5], [300, 90]),
+    ("fp32", 32, 1, 128, 32, 16, 3, [2], [80]),
+]
+
+
+def _run(qsa, case, seed=11, std=1.0, poison=NAN, lead=1, tail=2):
+    dtype, Hq, Hkv, d, page, block, topk, q_len, kv_len = case
+    dt = DT[dtype]
+    g = U.make_batch(q_len, kv_len, page, seed=seed, lead=lead, tail=tail)
+    cfg = _cfg(qsa, Hq, Hkv, d, block=block, topk=max(topk, 1), dtype=dtype)
+    kp, vp = U.pools(Hkv, d, g, kv_len, dt, seed=seed + 1, std=std, poison=poison)
+    gen = torch.Generator().manual_seed(seed + 2)
+    q = torch.full((g["n_tok"], Hq, d), NAN)
+    q[lead:g["n_tok"] - tail] = torch.randn(sum(q_len), Hq, d, generator=gen)
+    q = q.to(dt).cuda()
+    sel = None
+    if topk:
+        sel = torch.full((g["n_tok"], topk), 12345, dtype=torch.int32)
+        sel[lead:g["n_tok"] - tail] = U.selection(q_len, kv_len, block, topk, seed + 3)
+        sel = sel.cuda()
+    pg = qsa.make_paged(**g)
+    out = torch.full_like(q, 7.0)
+    ws = qsa.alloc_paged_workspace(cfg, pg)
+    return dict(cfg=cfg, pg=pg, q=q, kp=kp, vp=vp, sel=sel, out=out, ws=ws, g=g, rows=slice(lead, g["n_tok"] - tail))
+
+
+def _attn(qsa, s, stream=None):
+    qsa.qsa_paged_attn(s["cfg"], s["pg"], s["q"], s["kp"], s["vp"], s["sel"], s["out"], s["ws"], stream=stream)
+
+
+def _oracle(s, case):
+    dtype, Hq, Hkv, d, page, block, topk, q_len, kv_len = case
+    r = s["rows"]
+    return U.attention(s["q"][r], s["kp"], s["vp"], s["g"]["page_table"], q_len, kv_len, 1 / math.sqrt(d), block,
+                       None if s["sel"] is None else s["sel"][r])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c[:7]) + f"-q{max(c[7])}")
+def test_attention(cuda_lib, case):
+    qsa = cuda_lib
+    s = _run(qsa, case)
+    _attn(qsa, s)
+    assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK
+    U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+    assert (s["out"][:1] == 7).all() and (s["out"][-2:] == 7).all()  # rows of no sequence
+    first = s["out"].clone()
+    s["out"].fill_(7.0)
+    _attn(qsa, s)  # the workspace is as it was: the same bits again
+    assert torch.equal(first, s["out"])
+    assert int(s["ws"][:256].sum()) == 0
