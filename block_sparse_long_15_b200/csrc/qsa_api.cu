@@ -534,6 +534,12 @@ qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRop
   return QSA_OK;
 }
 
+constexpr int kChunkRows = 64;
+bool paged_chunks(const Dims &D, const Paged &G) { return D.bf16 && (long long)G.max_chunk * D.G >= kChunkRows; }
+size_t paged_scratch(const Dims &D, const Paged &G) {
+  return round256(paged_rows_workspace(D)) + (paged_chunks(D, G) ? round256(paged_tc_workspace()) : 0);
+}
+
 // A packed tensor of rows of `width` elements, `row` elements apart.
 bool rows_ok(const Dims &D, const void *p, long long row, long long width) {
   return p && aligned16(p) && row >= width && row % (D.bf16 ? 8 : 4) == 0;
@@ -616,7 +622,7 @@ qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t
   if (s != QSA_OK) return s;
   if (!bytes) return QSA_ERR_INVALID_ARG;
   if ((s = resolve_paged(pg, &G)) != QSA_OK) return s;
-  *bytes = kStatusBytes + round256(paged_rows_workspace(D));
+  *bytes = kStatusBytes + paged_scratch(D, G);
   return QSA_OK;
 }
 
@@ -635,9 +641,20 @@ qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, cons
   const void *ptrs[] = {q, k_pages, v_pages, sel, out, workspace};
   for (const void *p : ptrs)
     if (!aligned16(p)) return QSA_ERR_INVALID_ARG;
-  if (workspace_bytes < kStatusBytes + paged_rows_workspace(D)) return QSA_ERR_INVALID_ARG;
-  return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, (char *)workspace + kStatusBytes,
-                                       status_word(workspace), (cudaStream_t)stream));
+  if (workspace_bytes < kStatusBytes + paged_scratch(D, G)) return QSA_ERR_INVALID_ARG;
+  char *scratch = (char *)workspace + kStatusBytes;
+  int *status = status_word(workspace);
+  cudaStream_t st = (cudaStream_t)stream;
+  // Sequences with kChunkRows or more (token, head) rows go to the tensor-core kernel where it
+  // serves the shape, the others to the row kernel.
+  long long rows_below = 1LL << 62;
+  if (paged_chunks(D, G) && paged_tc_supported(D, G, sel != nullptr)) {
+    s = cuda_status(launch_paged_tc(D, G, q, k_pages, v_pages, sel, out, kChunkRows,
+                                    scratch + round256(paged_rows_workspace(D)), status, st));
+    if (s != QSA_OK) return s;
+    rows_below = kChunkRows;
+  }
+  return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, rows_below, scratch, status, st));
 }
 
 qsa_status_t qsa_read_device_status(void *workspace, qsa_stream_t stream, qsa_status_t *status) {

@@ -61,6 +61,7 @@ struct RowsParams {
   int tpb;        // tiles per selected block
   int rtk;        // units per token and KV head with a selection: ceil(G / R)
   int b0, nb;     // the sequences of this launch
+  long long max_rows;  // sequences with as many (token, head) rows are left out
 };
 
 // ---------------------------------------------------------------- the list of items
@@ -82,7 +83,8 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
   const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
   long long run = 0;
   for (int b = a; b < z; ++b) {
-    const PagedSeq s = paged_seq(P.P, P.b0 + b, P.status);
+    PagedSeq s = paged_seq(P.P, P.b0 + b, P.status);
+    if ((long long)s.n * P.G >= P.max_rows) s.n = 0;
     int rt, tiles;
     if (P.sel) {
       rt = s.n * P.rtk;
@@ -761,7 +763,8 @@ size_t paged_rows_workspace(const Dims &D) {
 }
 
 cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
-                              const int32_t *sel, void *out, void *scratch, int *status, cudaStream_t st) {
+                              const int32_t *sel, void *out, long long max_rows, void *scratch, int *status,
+                              cudaStream_t st) {
   RowsParams P;
   P.Hq = D.Hq;
   P.Hkv = D.Hkv;
@@ -780,8 +783,9 @@ cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, cons
   P.part_o = (float *)((char *)scratch + (size_t)kMaxCtas * sizeof(int));
   P.part_ml = P.part_o + (size_t)2 * kMaxCtas * kMaxRows * D.d;
   P.status = status;
+  P.max_rows = max_rows;
   P.tpb = (D.B + kTile - 1) / kTile;
-  const long long rows = sel ? D.G : (long long)D.G * G.max_chunk;
+  const long long rows = sel ? D.G : std::min((long long)D.G * G.max_chunk, max_rows - 1);
   const bool mma = D.bf16 && (D.d == 64 || D.d == 128 || D.d == 256) && (!sel || D.B % kTile == 0);
   P.R = mma && rows <= 8 ? 8 : kMaxRows;
   P.rtk = (D.G + P.R - 1) / P.R;
