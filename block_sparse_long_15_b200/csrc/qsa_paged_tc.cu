@@ -17,13 +17,16 @@
 // the last unit of a range are shared with neighbours. A part of a unit leaves its
 // unnormalised O with (m, l) per row in the workspace, two slots per CTA, and k_paged_merge,
 // one row a warp, joins them in order. Inside a CTA the roles are pipelined across units:
-//   warp 18     builder: the next unit's geometry, selection lists and chunk bitmaps;
 //   warp 0      TMA producer: Q, then K of chunk j and V of chunk j - 1 into ring entry j;
 //               its lanes hold the page numbers of the next chunk's boxes;
 //   warp 1      MMA issuer (TMEM owner): per chunk O_A += P_A V, S_A = Q_A K'^T, then B;
-//   warps 2-17  softmax, eight per tile, 16 rows per warp, two threads a row (16x32bx2 TMEM
-//               accesses): row max, P in bf16 over the first half of each S half, O rescaled
-//               only when the max has moved by more than 2^8, and the epilogue.
+//   warp 2      builder: the next unit's geometry, selection lists and chunk bitmaps;
+//   warps 4-19  softmax, eight per tile, 16 rows per warp, two threads a row with 64 logits
+//               each in registers (16x32bx2 TMEM accesses): row max by one shuffle, P in bf16
+//               over the first half of each S half, in two steps that the PV product takes
+//               as they come, O rescaled only when the max has moved by more than 2^8, and
+//               the epilogue. Four warps a scheduler: with one thread a row the exponentials
+//               and the arithmetic around them did not overlap (1560-1610 us at 8K of 32K).
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
 #include <cuda.h>
 #include <math.h>
@@ -42,10 +45,11 @@ constexpr int kD = 128;      // head dim served
 constexpr int kRows = 128;   // MMA M: (token, head) rows per tile
 constexpr int kTiles = 2;    // tiles per unit
 constexpr int kChunk = 128;  // keys per chunk
-constexpr int kHalf = 64;    // keys a softmax thread holds of a chunk; smallest block size served
+constexpr int kHalf = 64;    // mask granularity: the smallest block size served
 constexpr int kNE = 2;       // ring depth: entry j holds K of chunk j and V of chunk j - 1
-constexpr int kThreads = 608;
-constexpr int kBuilderWarp = 18;
+constexpr int kThreads = 640;
+constexpr int kBuilderWarp = 2;
+constexpr int kSoftWarp0 = 4;  // first softmax warp
 constexpr int kSoftWarps = 16;
 constexpr uint32_t kTmemCols = 512;  // S of tile w at 128 w, O of tile w at 256 + 128 w
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -56,14 +60,16 @@ constexpr int kMinKeys = 512;    // keys of a unit that make a CTA's range worth
 constexpr uint32_t kQBytes = kRows * kD * 2;    // per tile, two 64-column halves
 constexpr uint32_t kKVBytes = kChunk * kD * 2;  // per K (or V) chunk, two halves
 constexpr uint32_t kEntryBytes = 2 * kKVBytes;
-constexpr uint32_t kSelSlotBytes = 8192;        // a unit's selection lists, if they fit
+constexpr int kBitWords = 2048;                 // words of a segment's token bits: 2 a chunk and token
+constexpr int kBitTileWords = 128;              // and of its tiles' bits
+constexpr uint32_t kBitSlotBytes = (kBitWords + kBitTileWords) * 4;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffE = kOffQ + kTiles * kQBytes;
 constexpr uint32_t kOffBar = kOffE + kNE * kEntryBytes;
 constexpr uint32_t kOffMisc = kOffBar + 256;
 constexpr uint32_t kOffInfo = kOffMisc + 64;
 constexpr uint32_t kInfoBytes = 64;
-constexpr uint32_t kOffSel = kOffInfo + 2 * kInfoBytes;
+constexpr uint32_t kOffBits = kOffInfo + 2 * kInfoBytes;  // with a selection: [slot] kBitSlotBytes
 
 // barrier slots
 constexpr int kBarQ = 0;                        // Q of the unit landed
@@ -71,12 +77,11 @@ constexpr int kBarQEmpty = 1;                   // every QK of the unit complete
 constexpr int kBarFull = 2;                     // [ring entry]
 constexpr int kBarEmpty = kBarFull + kNE;       // [ring entry]
 constexpr int kBarSFull = kBarEmpty + kNE;      // [tile]
-constexpr int kBarPFull = kBarSFull + 2;        // [tile], 8 arrivals
-constexpr int kBarPVDone = kBarPFull + 2;       // [tile]
+constexpr int kBarPFull = kBarSFull + 2;        // [tile][step], 8 arrivals
+constexpr int kBarPVDone = kBarPFull + 4;       // [tile]
 constexpr int kBarSlotFull = kBarPVDone + 2;    // [slot], the builder's 32 lanes
 constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
-constexpr int kBarSel = kBarSlotFree + 2;       // the builder's bulk copy of a unit's lists
-constexpr int kNumBars = kBarSel + 1;
+constexpr int kNumBars = kBarSlotFree + 2;
 static_assert(kNumBars * 8 <= 256, "barrier area");
 
 struct TcParams {
@@ -88,11 +93,12 @@ struct TcParams {
   float *part_ml;      // [2 C][kTiles * kRows][2]
   int *status;
   int T;               // tokens per tile
+  float sl2;           // scale * log2(e)
   int C;               // CTAs
   int b0, nb;          // sequences of this launch
   int min_rows;        // sequences with fewer (token, head) rows are left to the row kernel
   int box;             // keys per TMA box: min(page size, kChunk)
-  int bitmap_words;    // capacity of a chunk bitmap
+  int W;               // words of 16 chunks a token's bits have
 };
 
 // ---------------------------------------------------------------- the key list
@@ -199,29 +205,36 @@ struct UnitInfo {
   int live;  // 0: no segment left
   int b, g, q0, r0, n, len;
   int slot;  // partial slot, -1: the whole unit
-  int nwords;
+  int ca, cb;     // chunks [ca, cb)
+  int cend[2];    // without a selection tile w sees the chunks below cend[w]
+  int part;       // bit 0: the first of the unit's segments here, bit 1: the last
 };
 static_assert(sizeof(UnitInfo) <= kInfoBytes, "unit info area");
 
-// Smallest set bit >= c in (bm0 | bm1), or -1.
-__device__ __forceinline__ int next_chunk(const uint32_t *bm0, const uint32_t *bm1, int nwords, int c) {
-  int w = c >> 5;
-  if (w >= nwords) return -1;
-  uint32_t bits = (bm0[w] | bm1[w]) & (0xffffffffu << (c & 31));
-  while (true) {
-    if (bits) return (w << 5) + __ffs(bits) - 1;
-    if (++w >= nwords) return -1;
-    bits = bm0[w] | bm1[w];
+// The chunks of a segment: of the unit (the union of its tiles') and of each tile. With a
+// selection bit 2 i + h of a bit list stands for half h of chunk ca + i.
+template <bool kSel>
+struct Chunks {
+  const uint32_t *bits;  // tile 0's words, then tile 1's
+  int nw, ca, cend[2];
+  __device__ __forceinline__ Chunks(const UnitInfo &I, const uint32_t *tile_bits, int W)
+      : bits(tile_bits), nw(W), ca(I.ca), cend{I.cend[0], I.cend[1]} {}
+  // Smallest chunk >= c of the unit, or -1.
+  __device__ __forceinline__ int next(int c) const {
+    if (!kSel) return c < max(cend[0], cend[1]) ? c : -1;
+    int w = (c - ca) >> 4;
+    if (w >= nw) return -1;
+    uint32_t x = (bits[w] | bits[nw + w]) & (0xffffffffu << (2 * ((c - ca) & 15)));
+    while (true) {
+      if (x) return ca + (w << 4) + ((__ffs(x) - 1) >> 1);
+      if (++w >= nw) return -1;
+      x = bits[w] | bits[nw + w];
+    }
   }
-}
-__device__ __forceinline__ bool bit_of(const uint32_t *bm, int c) { return (bm[c >> 5] >> (c & 31)) & 1u; }
-// The bits of word w that lie in [lo, hi).
-__device__ __forceinline__ uint32_t span_word(int w, int lo, int hi) {
-  const int a = max(lo - 32 * w, 0), z = min(hi - 32 * w, 32);
-  if (a >= z) return 0u;
-  return (z == 32 ? 0xffffffffu : (1u << z) - 1u) & ~((1u << a) - 1u);
-}
-
+  __device__ __forceinline__ bool has(int w, int c) const {
+    return kSel ? (bits[w * nw + ((c - ca) >> 4)] >> (2 * ((c - ca) & 15))) & 3u : c < cend[w];
+  }
+};
 // A wait taken by a whole warp: the same answer on every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
@@ -240,32 +253,32 @@ __device__ __forceinline__ bool idle_wait_warp(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// P for one 32-key quarter held in registers (fp32 bits), written back in place over
-// sv[0 .. 15] as bf16 pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on.
-// Returns the quarter's sum (of the fp32 values: only the product with V sees them in bf16).
+// P for 32 keys held in registers (fp32 bits), written back in place over sv[0 .. 15] as bf16
+// pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds them to acc (the
+// fp32 values: only the product with V sees them in bf16).
 template <bool kAll>
-__device__ __forceinline__ float p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2) {
-  uint64_t acc0 = 0, acc1 = 0;
+__device__ __forceinline__ void p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2, uint64_t (&acc)[2]) {
 #pragma unroll
   for (int u = 0; u < 32; u += 2) {
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(sv[u], sv[u + 1]), scale2, negm2), x0, x1);
-    float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    float p0, p1;
+    f2_unpack(f2_fma(f2_pack(sv[u], sv[u + 1]), scale2, negm2), p0, p1);
+    p0 = ex2_approx(p0);
+    p1 = ex2_approx(p1);
     if (!kAll) {
       p0 = (u < lim) ? p0 : 0.f;
       p1 = (u + 1 < lim) ? p1 : 0.f;
     }
     sv[u >> 1] = pack_bf16x2(p0, p1);
-    if ((u >> 1) & 1) acc1 = f2_add(acc1, f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-    else acc0 = f2_add(acc0, f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+    acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
   }
-  float s0, s1;
-  f2_unpack(f2_add(acc0, acc1), s0, s1);
-  return s0 + s1;
+}
+__device__ __forceinline__ void zero_quarter(uint32_t (&sv)[32]) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) sv[u] = 0u;
 }
 // Max of the first `lim` of 32 fp32 values.
 template <bool kAll>
-__device__ __forceinline__ float max_quarter(const uint32_t *sv, int lim) {
+__device__ __forceinline__ float max_quarter(const uint32_t (&sv)[32], int lim) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int u = 0; u < 32; u += 8)
@@ -278,24 +291,51 @@ __device__ __forceinline__ float max_quarter(const uint32_t *sv, int lim) {
   return max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
 }
 
+// This thread's index, opaque to the compiler: what is derived from it is computed where it is
+// used instead of being kept in registers across the softmax loop. (Shared memory leaves almost
+// no L1, so a register that spills there costs a trip to L2 per chunk.)
+__device__ __forceinline__ int fresh_tid() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return t;
+}
+
+// A softmax thread's place: warp (tile w, lane group, sub-group) owns 16 rows of its tile; lane
+// t < 16 holds its row's first 64 keys of every chunk and the first 64 columns of its O, lane
+// t + 16 the same row's others.
+struct SoftPlace {
+  int w, row0, hh, row, tok, h;  // tile, the warp's first row, half, row, token of the unit, head of the group
+  bool in_tile;                  // G need not divide 128
+};
+__device__ __forceinline__ SoftPlace soft_place(int tid, int T, int G) {
+  SoftPlace p;
+  const int warp = tid >> 5, lane = tid & 31, sw = warp - kSoftWarp0;
+  p.w = sw >> 3;
+  p.row0 = 32 * (warp & 3) + 16 * ((sw >> 2) & 1);
+  p.hh = lane >> 4;
+  p.row = p.row0 + (lane & 15);
+  p.tok = p.w * T + p.row / G;
+  p.h = p.row % G;
+  p.in_tile = p.row / G < T;
+  return p;
+}
+
 // ---------------------------------------------------------------- builder
-// Kept out of line: its registers do not add to the softmax loop's.
-__device__ __noinline__ void build_segments(const TcParams &P, uint8_t *base, uint32_t *bitmaps, const long long *pre,
-                                            int lane) {
+template <bool kSel>
+__device__ __forceinline__ void build_segments(const TcParams &P, uint8_t *base, const long long *pre, int lane) {
   uint64_t *bars = (uint64_t *)(base + kOffBar);
   volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
-  const int T = P.T, k = P.D.k, B = P.D.B, bw = P.bitmap_words;
-  const bool sel_cached = kTiles * T * k * 4 <= (int)kSelSlotBytes;
+  const int T = P.T, k = P.D.k, B = P.D.B, W = P.W;
   const long long total = pre[P.nb];
   const int C = ctas_of(P, total), c = blockIdx.x;
   long long x = c < C ? range_start(P, pre, total, C, c) : total;
   const long long lo = x, hi = c < C ? range_start(P, pre, total, C, c + 1) : total;
-  bool fail = false;
-  int n_bulk = 0;
+  int sub = -1;  // with a selection: first chunk of the unit's next segment; the bits of one have room for 16 W
   for (int su = 0;; ++su) {
     const int s = su & 1;
     if (su >= 2 && !idle_wait_warp(&bars[kBarSlotFree + s], ((su >> 1) - 1) & 1)) {
-      fail = true;
+      if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
+      *abort_flag = 1;
       break;
     }
     UnitInfo &I = *(UnitInfo *)(base + kOffInfo + s * kInfoBytes);
@@ -307,69 +347,39 @@ __device__ __noinline__ void build_segments(const TcParams &P, uint8_t *base, ui
     }
     const Unit r = unit_at(P, pre, x);
     const long long end = min(hi, r.first + r.w);
-    const int ca = (int)((x - r.first) / kChunk), cb = (int)((end - r.first + kChunk - 1) / kChunk);
+    const int c_lo = (int)((x - r.first) / kChunk), c_hi = (int)((end - r.first + kChunk - 1) / kChunk);
+    const int ca = sub >= 0 ? sub : c_lo, cb = kSel ? min(c_hi, ca + 16 * W) : c_hi;
     const int r0 = r.u * kTiles * T, n = r.q.s.n, t0 = r.q.s.len - n;
-    uint32_t *bm0 = bitmaps + (s * kTiles) * bw, *bm1 = bm0 + bw;
-    const int nwords = (cb + 31) >> 5;
-    if (!P.sel) {
-      // every chunk up to the tile's last token
-      const int c0 = min(cb, (t0 + min(n, r0 + T) - 1) / kChunk + 1);
-      const int c1 = r0 + T < n ? min(cb, (t0 + min(n, r0 + 2 * T) - 1) / kChunk + 1) : 0;
-      for (int w = lane; w < nwords; w += 32) {
-        bm0[w] = span_word(w, ca, c0);
-        bm1[w] = span_word(w, ca, c1);
-      }
-    } else {
-      int32_t *sel_s = (int32_t *)(base + kOffSel + s * kSelSlotBytes);
-      for (int w = lane; w < nwords; w += 32) bm0[w] = bm1[w] = 0;
-      __syncwarp();
-      // The unit's lists are one contiguous range: one bulk copy when it is aligned and fits.
-      const int rows = min(kTiles * T, n - r0);
-      const int32_t *src = P.sel + ((size_t)r.q.s.q0 + r0) * k;
-      const uint32_t bytes = (uint32_t)(rows * k * 4);
-      const bool bulk = sel_cached && ((reinterpret_cast<uintptr_t>(src) | bytes) & 15) == 0;
-      if (bulk) {
-        if (lane == 0) {
-          fence_proxy_async_smem();  // the slot's last readers were generic-proxy loads
-          mbar_arrive_expect_tx(&bars[kBarSel], bytes);
-          bulk_load(sel_s, src, bytes, &bars[kBarSel]);
-        }
-        const bool got = warp_wait(&bars[kBarSel], n_bulk & 1);
-        ++n_bulk;
-        if (!got) {
-          fail = true;
-          break;
-        }
-      } else if (sel_cached) {
-        for (int e = lane; e < rows * k; e += 32) sel_s[e] = src[e];
-        __syncwarp();
-      }
-      const int32_t *lists = sel_cached ? sel_s : src;
-      for (int tok = lane; tok < rows; tok += 32) {
+    if (kSel) {
+      uint32_t *bits = (uint32_t *)(base + kOffBits + s * kBitSlotBytes), *tile_bits = bits + kBitWords;
+      const int rows = min(kTiles * T, n - r0), h0 = 2 * ca, h1 = 2 * cb, per = B / kHalf;
+      // A token's bits, one token a lane: the halves of its selected blocks (an ascending list) and
+      // of its trailing range
+      for (int tok = lane; tok < kTiles * T; tok += 32) {
+        uint32_t *mine = bits + tok * W;
+        for (int i = 0; i < W; ++i) mine[i] = 0;
+        if (tok >= rows) continue;
         const int t = t0 + r0 + tok, n_c = (t + 1) / B;
-        uint32_t *bm = tok < T ? bm0 : bm1;
-        uint32_t word = 0;  // the bits of one word are gathered and set at once
-        int wi = -1;
-        auto set = [&](int ch) {
-          if (ch < ca || ch >= cb) return;
-          if ((ch >> 5) != wi) {
-            if (wi >= 0) atomicOr(&bm[wi], word);
-            wi = ch >> 5;
-            word = 0;
-          }
-          word |= 1u << (ch & 31);
+        const int32_t *list = P.sel + ((size_t)r.q.s.q0 + r0 + tok) * k;
+        auto set = [&](int a, int z) {
+          for (int h = max(a, h0); h < min(z, h1); ++h) mine[(h - h0) >> 5] |= 1u << ((h - h0) & 31);
         };
+#pragma unroll 4
         for (int i = 0; i < k; ++i) {
-          const int j = lists[tok * k + i];
-          if (j < 0 || j >= n_c) continue;
-          for (int ch = j * B / kChunk; ch <= (j * B + B - 1) / kChunk; ++ch) set(ch);
+          const int j = list[i];
+          if (j >= 0 && j < n_c) set(j * per, j * per + per);
         }
-        if (n_c * B <= t)
-          for (int ch = n_c * B / kChunk; ch <= t / kChunk; ++ch) set(ch);
-        if (wi >= 0) atomicOr(&bm[wi], word);
+        set(n_c * per, t / kHalf + 1);
       }
+      __syncwarp();
+      for (int e = lane; e < kTiles * W; e += 32) {
+        const int w = e / W, i = e - w * W;
+        uint32_t any = 0;
+        for (int tok = 0; tok < T; ++tok) any |= bits[(w * T + tok) * W + i];
+        tile_bits[e] = any;
+      }
+      __syncwarp();
     }
-    __syncwarp();
     if (lane == 0) {
       I.b = P.b0 + r.b;
       I.g = r.g;
@@ -377,20 +387,23 @@ __device__ __noinline__ void build_segments(const TcParams &P, uint8_t *base, ui
       I.r0 = r0;
       I.n = n;
       I.len = r.q.s.len;
-      I.slot = ca == 0 && end == r.first + r.w ? -1 : 2 * c + (x == lo ? 0 : 1);
-      I.nwords = nwords;
+      I.slot = c_lo == 0 && end == r.first + r.w ? -1 : 2 * c + (x == lo ? 0 : 1);
+      I.ca = ca;
+      I.cb = cb;
+      // every chunk up to the tile's last token
+      I.cend[0] = min(cb, (t0 + min(n, r0 + T) - 1) / kChunk + 1);
+      I.cend[1] = r0 + T < n ? min(cb, (t0 + min(n, r0 + 2 * T) - 1) / kChunk + 1) : ca;
+      I.part = (ca == c_lo ? 1 : 0) | (cb == c_hi ? 2 : 0);
       I.live = 1;
     }
     __syncwarp();
     mbar_arrive(&bars[kBarSlotFull + s]);
-    x = end;
-  }
-  if (fail) {
-    if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
-    *abort_flag = 1;
+    if (cb == c_hi) x = end, sub = -1;
+    else sub = cb;
   }
 }
 
+template <bool kSel>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcParams P) {
@@ -399,20 +412,18 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   uint64_t *bars = (uint64_t *)(base + kOffBar);
   uint32_t *tmem_slot = (uint32_t *)(base + kOffMisc);
   volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
-  long long *pre = (long long *)(base + kOffSel + (P.sel ? 2 * kSelSlotBytes : 0));
-  uint32_t *bitmaps = (uint32_t *)(pre + P.nb + 1);  // [slot][tile][bitmap_words]
+  long long *pre = (long long *)(base + kOffBits + (kSel ? 2 * kBitSlotBytes : 0));
 
   const Dims &D = P.D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int T = P.T, G = D.G, k = D.k, B = D.B, bw = P.bitmap_words;
-  const bool sel_cached = kTiles * T * k * 4 <= (int)kSelSlotBytes;
+  const int T = P.T, G = D.G;
   auto info = [&](int s) { return (const UnitInfo *)(base + kOffInfo + s * kInfoBytes); };
-  auto bitmap = [&](int s, int w) { return bitmaps + (s * kTiles + w) * bw; };
+  auto token_bits = [&](int s) { return (const uint32_t *)(base + kOffBits + s * kBitSlotBytes); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kBarPFull || i == kBarPFull + 1) count = 8;
+      if (i >= kBarPFull && i < kBarPFull + 4) count = 8;
       if (i == kBarSlotFull || i == kBarSlotFull + 1) count = 32;
       if (i == kBarSlotFree || i == kBarSlotFree + 1) count = 2 + kSoftWarps;
       mbar_init(&bars[i], count);
@@ -436,7 +447,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   const uint32_t tbase = *tmem_slot;
 
   if (warp == kBuilderWarp) {
-    build_segments(P, base, bitmaps, pre, lane);
+    build_segments<kSel>(P, base, pre, lane);
   } else if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     // Lane i < 128 / box holds the pool plane (page, KV head) of the i-th box of the next chunk
@@ -444,7 +455,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int n_box = kChunk / P.box;
     const uint32_t box_bytes = (uint32_t)P.box * 128;  // 64 columns of a box
     int j = 0, qn = 0;
-    bool fail = false;
+    bool fail = false, have_q = false;
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
       if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
@@ -453,7 +464,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       }
       const UnitInfo I = *info(s);
       if (!I.live) break;
-      const uint32_t *bm0 = bitmap(s, 0), *bm1 = bitmap(s, 1);
+      if (I.part & 1) have_q = false;
+      const Chunks<kSel> ch(I, token_bits(s) + kBitWords, P.W);
       const int t_hi = I.len - I.n + min(I.n, I.r0 + kTiles * T) - 1;  // the unit's last visible key
       auto plane = [&](int c) {
         int z = -1;
@@ -465,24 +477,27 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         return z;
       };
-      int c = next_chunk(bm0, bm1, I.nwords, 0);
+      int c = ch.next(ch.ca);
       if (c >= 0) {
         int z = plane(c), zp = -1, cp = -1;  // boxes of K chunk c and of V chunk cp
-        if (qn > 0 && !warp_wait(&bars[kBarQEmpty], (qn - 1) & 1)) {
-          fail = true;
-          break;
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars[kBarQ], (uint32_t)(kTiles * 2 * T * G * 128));
-          for (int w = 0; w < kTiles; ++w) {
-            uint8_t *dst = base + kOffQ + w * kQBytes;
-            tma_load_3d(&tm_q, &bars[kBarQ], dst, 0, I.g * G, I.q0 + I.r0 + w * T);
-            tma_load_3d(&tm_q, &bars[kBarQ], dst + kQBytes / 2, 64, I.g * G, I.q0 + I.r0 + w * T);
+        if (!have_q) {
+          if (qn > 0 && !warp_wait(&bars[kBarQEmpty], (qn - 1) & 1)) {
+            fail = true;
+            break;
           }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars[kBarQ], (uint32_t)(kTiles * 2 * T * G * 128));
+            for (int w = 0; w < kTiles; ++w) {
+              uint8_t *dst = base + kOffQ + w * kQBytes;
+              tma_load_3d(&tm_q, &bars[kBarQ], dst, 0, I.g * G, I.q0 + I.r0 + w * T);
+              tma_load_3d(&tm_q, &bars[kBarQ], dst + kQBytes / 2, 64, I.g * G, I.q0 + I.r0 + w * T);
+            }
+          }
+          have_q = true;
+          ++qn;
         }
-        ++qn;
         while (c >= 0 || cp >= 0) {
-          const int cn = c >= 0 ? next_chunk(bm0, bm1, I.nwords, c + 1) : -1;
+          const int cn = c >= 0 ? ch.next(c + 1) : -1;
           const int zn = plane(cn);  // read ahead
           const int se = j % kNE;
           if (j >= kNE && !warp_wait(&bars[kBarEmpty + se], ((j / kNE) & 1) ^ 1)) {
@@ -511,10 +526,6 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           c = cn;
           z = zn;
           ++j;
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) {
-            fail = true;
-            break;
-          }
         }
       }
       __syncwarp();
@@ -531,6 +542,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     int j = 0, qn = 0;
     int n_pv0 = 0, n_pv1 = 0;  // PVs issued per tile
     bool fail = false;
+    // of the unit: its Q is there, its last QK is issued, the tile's next PV is its first
+    bool have_q = false, q_done = false, first0 = true, first1 = true;
     const uint64_t q_desc0 = sdesc_sw128(smem_u32(base + kOffQ), 16, 1024);
     const uint64_t k_desc0 = sdesc_sw128(smem_u32(base + kOffE), 16, 1024);
     const uint64_t v_desc0 = sdesc_sw128(smem_u32(base + kOffE + kKVBytes), kKVBytes / 2, 1024);
@@ -549,14 +562,20 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // O_w (+)= P_w V from ring entry se once P_w is written; a unit's first PV overwrites O
     auto issue_pv = [&](int w, int se, bool first) -> bool {
       const int cnt = w ? n_pv1++ : n_pv0++;
-      if (!warp_wait(&bars[kBarPFull + w], cnt & 1)) return false;
-      tc_fence_after();
       const uint64_t vd = v_desc0 + (uint64_t)((se * kEntryBytes) >> 4);
       const uint32_t o = tbase + 256u + (uint32_t)(w * 128), pcol = tbase + (uint32_t)(w * 128);
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk)
-        mma_ts_w(o, pcol + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                 (!first || kk > 0) ? 1u : 0u);
+      for (int step = 0; step < 2; ++step) {
+        if (!warp_wait(&bars[kBarPFull + 2 * w + step], cnt & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // keys 16 kk .. of half kk / 4 sit at columns 64 (kk / 4) + 8 (kk % 4); a step brings 32 keys of each
+          const int kk = (e >> 1) * 4 + step * 2 + (e & 1);
+          mma_ts_w(o, pcol + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                   (!first || step > 0 || e > 0) ? 1u : 0u);
+        }
+      }
       mma_commit_w(&bars[kBarPVDone + w]);
       return true;
     };
@@ -566,27 +585,33 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         fail = true;
         break;
       }
-      const int live = info(s)->live, nwords = info(s)->nwords;
+      const int live = info(s)->live, part = info(s)->part;
       const int t_hi = info(s)->len - info(s)->n + min(info(s)->n, info(s)->r0 + kTiles * T) - 1;
       if (!live) break;
-      const uint32_t *bm0 = bitmap(s, 0), *bm1 = bitmap(s, 1);
-      int c = next_chunk(bm0, bm1, nwords, 0);
+      if (part & 1) have_q = q_done = false, first0 = first1 = true;
+      const Chunks<kSel> ch(*info(s), token_bits(s) + kBitWords, P.W);
+      int c = ch.next(ch.ca);
       if (c >= 0) {
-        bool first0 = true, first1 = true;
-        if (!warp_wait(&bars[kBarQ], qn & 1)) fail = true;
-        ++qn;
-        tc_fence_after();
+        if (!have_q) {
+          if (!warp_wait(&bars[kBarQ], qn & 1)) fail = true;
+          ++qn;
+          have_q = true;
+          tc_fence_after();
+        }
         if (!fail) {
           const int se = j % kNE;
           if (!warp_wait(&bars[kBarFull + se], (j / kNE) & 1)) fail = true;
           tc_fence_after();
           for (int w = 0; w < kTiles && !fail; ++w)
-            if (bit_of(w ? bm1 : bm0, c)) issue_qk(w, se);
+            if (ch.has(w, c)) issue_qk(w, se);
           if (!fail) mma_commit_w(&bars[kBarEmpty + se]);
           ++j;
         }
-        int cn = fail ? -1 : next_chunk(bm0, bm1, nwords, c + 1);
-        if (!fail && cn < 0) mma_commit_w(&bars[kBarQEmpty]);
+        int cn = fail ? -1 : ch.next(c + 1);
+        if (!fail && cn < 0 && (part & 2)) {
+          mma_commit_w(&bars[kBarQEmpty]);
+          q_done = true;
+        }
         while (!fail && c >= 0) {
           const int se = j % kNE;
           if (!warp_wait(&bars[kBarFull + se], (j / kNE) & 1)) {
@@ -609,25 +634,28 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             __syncwarp();
           }
           for (int w = 0; w < kTiles; ++w) {
-            if (bit_of(w ? bm1 : bm0, c)) {
+            if (ch.has(w, c)) {
               if (!issue_pv(w, se, w ? first1 : first0)) {
                 fail = true;
                 break;
               }
               (w ? first1 : first0) = false;
             }
-            if (cn >= 0 && bit_of(w ? bm1 : bm0, cn)) issue_qk(w, se);
+            if (cn >= 0 && ch.has(w, cn)) issue_qk(w, se);
           }
           if (fail) break;
           mma_commit_w(&bars[kBarEmpty + se]);
           ++j;
-          const int cnn = cn >= 0 ? next_chunk(bm0, bm1, nwords, cn + 1) : -1;
-          if (cn >= 0 && cnn < 0) mma_commit_w(&bars[kBarQEmpty]);
+          const int cnn = cn >= 0 ? ch.next(cn + 1) : -1;
+          if (cn >= 0 && cnn < 0 && (part & 2)) {
+            mma_commit_w(&bars[kBarQEmpty]);
+            q_done = true;
+          }
           c = cn;
           cn = cnn;
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) fail = true;
         }
       }
+      if (!fail && (part & 2) && have_q && !q_done) mma_commit_w(&bars[kBarQEmpty]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
     }
@@ -635,21 +663,15 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       record_status(P.status, QSA_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-  } else {
+  } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------- softmax + epilogue
-    const int sw = warp - 2;
-    const int w = sw >> 3;          // tile
-    const int sub = (sw >> 2) & 1;  // which 16 of the lane group's 32 rows
-    const int lg = warp & 3;        // TMEM lane group
-    const int hh = lane >> 4;       // this thread's 64-key half of every chunk, and 64 columns of O
-    const int row = 32 * lg + 16 * sub + (lane & 15);
-    const int tok = w * T + row / G, h = row % G;
-    const bool in_tile = row / G < T;  // G need not divide 128
-    const uint32_t lane_addr = tbase + ((uint32_t)(32 * lg + 16 * sub) << 16);
-    const uint32_t s_col = lane_addr + (uint32_t)(w * 128);
-    const uint32_t o_col = lane_addr + 256u + (uint32_t)(w * 128);
-    const float sl2 = D.scale * 1.4426950408889634f;
-    int n_all = 0;  // chunks of this tile over all segments so far: S, P and PV phases
+    const int w = (warp - kSoftWarp0) >> 3;  // tile
+    const uint32_t s_col = tbase + ((uint32_t)(32 * (warp & 3) + 16 * (((warp - kSoftWarp0) >> 2) & 1)) << 16) + w * 128;
+    const uint32_t o_col = s_col + 256;
+    const uint64_t scale2 = f2_splat(P.sl2);
+    int n_all = 0;      // chunks of this tile over all units so far: S, P and PV phases
+    bool some = false;  // a chunk of this unit
+    float m_ref = -INFINITY, l = 0.f;
     bool fail = false;
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
@@ -659,57 +681,69 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       }
       const UnitInfo *I = info(s);
       if (!I->live) break;
-      const uint32_t *bm0 = bitmap(s, 0), *bm1 = bitmap(s, 1);
-      const uint32_t *bm = w ? bm1 : bm0;
-      const int nwords = I->nwords;
-      const int t_last = I->len - I->n + min(I->n, I->r0 + kTiles * T) - 1;  // the unit's last visible key
-      const bool valid = in_tile && I->r0 + tok < I->n;
-      const int t = I->len - I->n + I->r0 + tok;  // this row's position
-      const int n_c = valid && P.sel ? (t + 1) / B : 0;
-      const int32_t *srow = sel_cached ? (const int32_t *)(base + kOffSel + s * kSelSlotBytes) + tok * k
-                                       : P.sel + ((size_t)I->q0 + (valid ? I->r0 + tok : 0)) * k;
-      float m_ref = -INFINITY, l = 0.f;
-      int ptr = 0, n = 0;
-      for (int c = next_chunk(bm0, bm1, nwords, 0); c >= 0; c = next_chunk(bm0, bm1, nwords, c + 1)) {
-        if (!bit_of(bm, c)) continue;
-        int lim = 0;  // this thread's first `lim` keys are visible
-        if (valid) {
-          const int key0 = c * kChunk + hh * kHalf;
-          const int jb = P.sel ? key0 / B : 0;
-          if (jb < n_c) {
-            while (ptr < k && (unsigned)srow[ptr] < (unsigned)jb) ++ptr;
-            lim = (ptr < k && srow[ptr] == jb) ? kHalf : 0;
-          } else {
-            lim = min(max(t + 1 - key0, 0), kHalf);
-          }
+      if (I->part & 1) {
+        some = false;
+        m_ref = -INFINITY;
+        l = 0.f;
+      }
+      const Chunks<kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      // A chunk whose last key is no further than t_free needs no mask per key: without a selection
+      // the position of the warp's first row, with one the unit's last visible key.
+      int t_free, t = 0, h_tail = 0;
+      const uint32_t *my_bits = nullptr;
+      {
+        const SoftPlace p = soft_place(fresh_tid(), T, G);
+        const int t0 = I->len - I->n + I->r0;
+        t_free = kSel ? t0 + min(I->n - I->r0, kTiles * T) - 1 : t0 + p.w * T + p.row0 / G;
+        if (kSel) {
+          const bool valid = p.in_tile && I->r0 + p.tok < I->n;
+          t = valid ? t0 + p.tok : -1;
+          h_tail = (t + 1) / D.B * (D.B / kHalf);  // the row's trailing range starts at this 64-key half
+          my_bits = token_bits(s) + (valid ? p.tok : 0) * P.W;
         }
-        const bool z = __all_sync(0xffffffffu, lim == 0);
-        // Keys are masked one by one only where a thread sees part of its half or the chunk
-        // reaches past the last visible key (NaN may be there). Elsewhere a thread sees all
-        // its keys or none; one that sees none takes +inf as its reference: p = 0.
-        const bool part = __any_sync(0xffffffffu, lim > 0 && lim < kHalf) || c * kChunk + kChunk - 1 > t_last;
+      }
+      for (int c = ch.next(ch.ca); c >= 0; c = ch.next(c + 1)) {
+        if (!ch.has(w, c)) continue;
+        // This thread's first `lim` keys are visible: without a selection, or in the trailing
+        // range, up to the position; else its half is a part of one block, seen whole or not.
+        // Keys are masked one by one where some row sees a part of its half, or behind the last
+        // visible key (NaN may be there). Elsewhere a thread sees all its keys or none; one that
+        // sees none takes +inf as its reference: p = 0.
+        int lim = kHalf;
+        bool part = c * kChunk + kChunk - 1 > t_free, any = true;
+        if (kSel) {
+          const int half = 2 * c + (lane >> 4);
+          lim = min(max(t + 1 - half * kHalf, 0), kHalf);
+          if (half < h_tail) lim = (my_bits[(c - ch.ca) >> 4] >> (half - 2 * ch.ca & 31)) & 1u ? kHalf : 0;
+          part = part || __any_sync(0xffffffffu, lim > 0 && lim < kHalf);
+          any = __any_sync(0xffffffffu, lim > 0);
+        } else if (part) {
+          const SoftPlace p = soft_place(fresh_tid(), T, G);
+          const bool valid = p.in_tile && I->r0 + p.tok < I->n;
+          lim = valid ? min(max(I->len - I->n + I->r0 + p.tok + 1 - (2 * c + p.hh) * kHalf, 0), kHalf) : 0;
+        }
         if (!warp_wait(&bars[kBarSFull + w], n_all & 1)) {
           fail = true;
           break;
         }
         tc_fence_after();
-        float hmax = -INFINITY;
-        if (!z) {
-          uint32_t sv0[32], sv1[32];
-          tmem_ld32_split<64>(s_col, sv0);
-          tmem_ld32_split<64>(s_col + 32, sv1);
+        // Logits come in 32 at a time, the second 32 twice (for the max, then for P): 64 of them in
+        // registers at once spill.
+        uint32_t sv[32];
+        float mx = -INFINITY;
+        if (any) {
+          tmem_ld32_split<64>(s_col + 32, sv);
           tmem_ld_wait();
-          if (part) {
-            hmax = fmaxf(max_quarter<false>(sv0, lim), max_quarter<false>(sv1, lim - 32));
-          } else {
-            const float mx = fmaxf(max_quarter<true>(sv0, 32), max_quarter<true>(sv1, 32));
-            hmax = lim ? mx : -INFINITY;
-          }
+          mx = part ? max_quarter<false>(sv, lim - 32) : max_quarter<true>(sv, 32);
+          tmem_ld32_split<64>(s_col, sv);
+          tmem_ld_wait();
+          mx = fmaxf(mx, part ? max_quarter<false>(sv, lim) : max_quarter<true>(sv, 32));
+          if (kSel && lim == 0) mx = -INFINITY;
         }
-        const float cmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 16)) * sl2;
+        const float cmax = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * P.sl2;
         bool rescale = false;
         float alpha = 1.f;
-        if (cmax > -INFINITY) {
+        if (cmax > -INFINITY) {  // the row sees a key here
           if (m_ref == -INFINITY) {
             m_ref = cmax;
           } else if (cmax > m_ref + 8.f) {
@@ -718,109 +752,102 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             m_ref = cmax;
           }
         }
-        float psum = 0.f;
-        if (z) {
-          uint32_t zk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) zk[e] = 0u;
-          tmem_st32_split<64>(s_col, zk);
-        } else {
-          const uint64_t scale2 = f2_splat(sl2);
-          const uint64_t negm2 = f2_splat(part || lim ? -m_ref : -INFINITY);
-          uint32_t sv0[32], sv1[32];
-          tmem_ld32_split<64>(s_col, sv0);
-          tmem_ld_wait();
-          psum = part ? p_quarter<false>(sv0, lim, scale2, negm2) : p_quarter<true>(sv0, 32, scale2, negm2);
-          tmem_ld32_split<64>(s_col + 32, sv1);
-          tmem_ld_wait();
-          psum += part ? p_quarter<false>(sv1, lim - 32, scale2, negm2) : p_quarter<true>(sv1, 32, scale2, negm2);
-          tmem_st32_split_lo<64>(s_col, sv0, sv1);
-        }
         if (__any_sync(0xffffffffu, rescale)) {
-          // O is stable once this tile's previous PV has completed, and the next one waits for
-          // this warp's arrival below
-          if (n >= 1 && !warp_wait(&bars[kBarPVDone + w], (n_all - 1) & 1)) {
+          // A row that had a reference had a chunk before. O is stable once that chunk's PV has
+          // completed, and the next one waits for this warp's arrivals below.
+          if (!warp_wait(&bars[kBarPVDone + w], (n_all - 1) & 1)) {
             fail = true;
             break;
           }
           tc_fence_after();
 #pragma unroll 1
-          for (int cb = 0; cb < 2; ++cb) {
-            uint32_t ov[32];
-            tmem_ld32_split<64>(o_col + cb * 32, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
-            tmem_st32_split<64>(o_col + cb * 32, ov);
-          }
-          l *= alpha;
-        }
-        l += psum;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarPFull + w]);
-        ++n;
-        ++n_all;
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) {
-          fail = true;
-          break;
-        }
-      }
-      const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both halves
-      // -------------------------------------------------------------- epilogue
-      // The segment's last PV of the tile is phase n_all - 1: the one before it completed
-      // before S of the last chunk did, and the next one needs this warp's next P.
-      bool have_o = false;
-      if (n > 0 && !fail) {
-        have_o = warp_wait(&bars[kBarPVDone + w], (n_all - 1) & 1);
-        if (!have_o) fail = true;
-      }
-      if (fail) {
-        if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      tc_fence_after();
-      const bool keep = lt > 0.f;  // a row that sees nothing is written as zeros
-      const int slot = I->slot;
-      if (slot < 0) {
-        const float inv = keep ? 1.f / lt : 0.f;
-        __nv_bfloat16 *orow =
-            P.out + (((size_t)I->q0 + (valid ? I->r0 + tok : 0)) * D.Hq + I->g * G + h) * kD + hh * 64;
-#pragma unroll 1
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t ov[16];
-          if (have_o) {
-            tmem_ld16_split<64>(o_col + cb * 16, ov);
-            tmem_ld_wait();
-          }
-          uint32_t pk[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            pk[q] = keep && have_o
-                        ? pack_bf16x2(__uint_as_float(ov[2 * q]) * inv, __uint_as_float(ov[2 * q + 1]) * inv)
-                        : 0u;
-          if (valid) {
-            uint4 *o4 = (uint4 *)(orow + cb * 16);
-            o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          }
-        }
-      } else {
-        const size_t pr = (size_t)slot * (kTiles * kRows) + w * kRows + row;
-        if (valid && hh == 0)
-          *(float2 *)(P.part_ml + pr * 2) = make_float2(have_o && keep ? m_ref : -INFINITY, keep ? lt : 0.f);
-        if (have_o) {
-#pragma unroll 1
           for (int cb = 0; cb < 4; ++cb) {
             uint32_t ov[16];
             tmem_ld16_split<64>(o_col + cb * 16, ov);
             tmem_ld_wait();
-            if (valid) {
-              uint4 *o4 = (uint4 *)(P.part_o + pr * kD + hh * 64 + cb * 16);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) o4[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-            }
+            for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
+            tmem_st16_split<64>(o_col + cb * 16, ov);
+          }
+          l *= alpha;
+        }
+        uint64_t acc[2] = {0, 0};
+        auto step_done = [&](int step) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarPFull + 2 * w + step]);
+        };
+        const uint64_t negm2 = f2_splat(!kSel || part || lim ? -m_ref : -INFINITY);
+        if (any) {
+          if (part) p_quarter<false>(sv, lim, scale2, negm2, acc);
+          else p_quarter<true>(sv, 32, scale2, negm2, acc);
+        } else {
+          zero_quarter(sv);
+        }
+        tmem_st16_split_lo<64>(s_col, sv);
+        if (any) {
+          tmem_ld32_split<64>(s_col + 32, sv);
+          tmem_ld_wait();
+        }
+        step_done(0);
+        if (any) {
+          if (part) p_quarter<false>(sv, lim - 32, scale2, negm2, acc);
+          else p_quarter<true>(sv, 32, scale2, negm2, acc);
+        }
+        tmem_st16_split_lo<64>(s_col + 16, sv);
+        float sum0, sum1;
+        f2_unpack(f2_add(acc[0], acc[1]), sum0, sum1);
+        l += sum0 + sum1;
+        step_done(1);
+        some = true;
+        ++n_all;
+      }
+      if ((I->part & 2) || fail) {
+        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both halves
+        // ------------------------------------------------------------ epilogue
+        // The unit's last PV of the tile is phase n_all - 1: the one before it completed
+        // before S of the last chunk did, and the next one needs this warp's next P.
+        bool have_o = false;
+        if (some && !fail) {
+          have_o = warp_wait(&bars[kBarPVDone + w], (n_all - 1) & 1);
+          if (!have_o) fail = true;
+        }
+        if (fail) {
+          if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        tc_fence_after();
+        const SoftPlace p = soft_place(fresh_tid(), T, G);
+        const bool valid = p.in_tile && I->r0 + p.tok < I->n;
+        const bool keep = have_o && lt > 0.f;  // a row that sees nothing is written as zeros
+        const int slot = I->slot;
+        const float inv = keep ? 1.f / lt : 0.f;
+        __nv_bfloat16 *orow =
+            P.out + (((size_t)I->q0 + (valid ? I->r0 + p.tok : 0)) * D.Hq + I->g * G + p.h) * kD + p.hh * 64;
+        const size_t pr = (size_t)max(slot, 0) * (kTiles * kRows) + w * kRows + p.row;
+        if (slot >= 0 && valid && p.hh == 0)
+          *(float2 *)(P.part_ml + pr * 2) = make_float2(keep ? m_ref : -INFINITY, keep ? lt : 0.f);
+#pragma unroll 1
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t ov[16];
+          __syncwarp();
+          if (have_o) {  // the same for the whole warp
+            tmem_ld16_split<64>(o_col + cb * 16, ov);
+            tmem_ld_wait();
+          }
+          if (valid && slot < 0) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              pk[q] = keep ? pack_bf16x2(__uint_as_float(ov[2 * q]) * inv, __uint_as_float(ov[2 * q + 1]) * inv) : 0u;
+            uint4 *o4 = (uint4 *)(orow + cb * 16);
+            o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          } else if (valid && have_o) {
+            uint4 *o4 = (uint4 *)(P.part_o + pr * kD + p.hh * 64 + cb * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o4[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
           }
         }
       }
@@ -918,22 +945,17 @@ bool make_map(CUtensorMap *m, const void *ptr, uint64_t d1, uint64_t d2, uint32_
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSmemMax = 227 * 1024;
-int bitmap_words_of(const Paged &G) {
-  const long long chunks = (((long long)G.max_pages << G.ps_shift) + kChunk - 1) / kChunk;
-  return (int)((chunks + 31) / 32);
+size_t smem_of(bool sel, int nb) {
+  return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + (size_t)(nb + 1) * 8;
 }
-size_t smem_of(const Paged &G, bool sel, int nb) {
-  return 1024 + kOffSel + (sel ? 2 * kSelSlotBytes : 0) + (size_t)(nb + 1) * 8 + (size_t)2 * kTiles * bitmap_words_of(G) * 4;
-}
+static_assert(1024 + kOffBits + 2 * kBitSlotBytes + (kMaxSeqs + 1) * 8 <= 227 * 1024, "shared memory");
 
 }  // namespace
 
-// bf16, head_dim 128, blocks of whole 64-key halves; a cache whose chunk bitmaps fit shared memory.
+// bf16, head_dim 128, blocks of whole 64-key halves.
 bool paged_tc_supported(const Dims &D, const Paged &G, bool sel) {
   return D.bf16 && D.d == kD && D.G <= 32 && (!sel || D.B % kHalf == 0) &&
-         (long long)G.n_pages * D.Hkv <= 0x7fffffffLL &&
-         smem_of(G, sel, std::min(G.batch, kMaxSeqs)) <= kSmemMax;
+         (long long)G.n_pages * D.Hkv <= 0x7fffffffLL;
 }
 
 size_t paged_tc_workspace() { return (size_t)2 * kMaxCtas * kTiles * kRows * (kD + 2) * sizeof(float); }
@@ -953,10 +975,11 @@ cudaError_t launch_paged_tc(const Dims &D, const Paged &G, const void *q, const 
   P.part_ml = P.part_o + (size_t)2 * kMaxCtas * kTiles * kRows * kD;
   P.status = status;
   P.T = kRows / D.G;
+  P.sl2 = D.scale * 1.4426950408889634f;
   P.C = std::min(sm_count(), kMaxCtas);
   P.min_rows = min_rows;
   P.box = std::min(G.ps, kChunk);
-  P.bitmap_words = bitmap_words_of(G);
+  P.W = std::min(kBitTileWords / kTiles, kBitWords / (kTiles * P.T));
   CUtensorMap tq, tk, tv;
   const uint64_t planes = (uint64_t)G.n_pages * D.Hkv;
   if (!make_map(&tq, q, D.Hq, G.n_tok, D.G, P.T) || !make_map(&tk, k_pages, G.ps, planes, P.box, 1) ||
@@ -966,11 +989,12 @@ cudaError_t launch_paged_tc(const Dims &D, const Paged &G, const void *q, const 
   }
   for (P.b0 = 0; P.b0 < G.batch; P.b0 += kMaxSeqs) {
     P.nb = std::min(kMaxSeqs, G.batch - P.b0);
-    const size_t smem = smem_of(G, sel != nullptr, P.nb);
-    cudaError_t e = ensure_smem(k_paged_tc, smem);
+    const size_t smem = smem_of(sel != nullptr, P.nb);
+    auto kern = sel ? k_paged_tc<true> : k_paged_tc<false>;
+    cudaError_t e = ensure_smem(kern, smem);
     if (e == cudaSuccess) {
       note_launch();
-      e = launch_maybe_pdl(k_paged_tc, dim3(P.C), dim3(kThreads), smem, st, false, tq, tk, tv, P);
+      e = launch_maybe_pdl(kern, dim3(P.C), dim3(kThreads), smem, st, false, tq, tk, tv, P);
     }
     if (e == cudaSuccess) {
       note_launch();

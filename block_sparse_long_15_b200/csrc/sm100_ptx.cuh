@@ -190,6 +190,14 @@ __device__ __forceinline__ void tmem_st16_split(uint32_t taddr, const uint32_t (
       ::"r"(taddr), "n"(kSplit), QSA_W8(0), QSA_W8(8)
       : "memory");
 }
+// 16x32bx2 store of r[0 .. 15] of a larger array (16 columns per thread).
+template <int kSplit>
+__device__ __forceinline__ void tmem_st16_split_lo(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};"
+      ::"r"(taddr), "n"(kSplit), QSA_W8(0), QSA_W8(8)
+      : "memory");
+}
 #define QSA_WB8(i) "r"(b[i]), "r"(b[i + 1]), "r"(b[i + 2]), "r"(b[i + 3]), "r"(b[i + 4]), "r"(b[i + 5]), \
                    "r"(b[i + 6]), "r"(b[i + 7])
 // 16x32bx2 store of a[0..15] then b[0..15] (32 columns per thread).
