@@ -6,12 +6,12 @@
 // in fp32, rounded once. Each element is read once and written once, with about 7
 // operations between: bound by HBM for a prompt, by latency for a decode step.
 //
-// A token is one CTA's work: its heads (of q, k, v and the indexer key) are cut into
-// rows of warp width, 8 elements (one or two 16-byte accesses) a lane, so a head of 128
-// sits in 16 lanes and a warp takes two at once. The mean of squares is a shuffle
-// reduction inside the head's lanes; the rotation partner of a lane's 8 elements is the
-// lane r/16 further on, whose raw values arrive by shuffle, so nothing but the token's
-// cosines and sines passes through shared memory.
+// A warp takes the heads of one token (or, with few tokens, a part of them: each of them then
+// computes the token's angles again). A head of d elements sits in d / 8 lanes, so a warp
+// holds 256 / d heads at once; a lane holds 4 elements i .. i + 3 and their rotation partners
+// i + r/2 .., as two 8-byte accesses, so the rotation needs no exchange, and the mean of
+// squares is the only shuffle. Norm weight, cosine and sine are multiplied once per token
+// and kind of head: out = rms (x_i (w_i c) - x_j (w_j s)), and so on.
 //
 // The angle is taken modulo a turn in integers: theta^(-2i/r) / 2 pi, as a 64-bit
 // fraction of a turn, times t wraps round exactly, and its upper 32 bits are the phase
@@ -19,15 +19,21 @@
 // position 65536 already.)
 #include <math.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "qsa_internal.h"
 #include "sm100_ptx.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBatch = 3;       // warp rows in flight per warp
+constexpr int kWarps = 4;
+// Warp rows in flight per warp: 16K rows of 32 + 4 heads of 128 take 61 us with 4, 57 with 6, 59
+// with 8; more warps with fewer registers each (8 or 10 blocks an SM) 61 to 68.
+constexpr int kBatch = 6;
 constexpr int kMaxHalf = 128;   // rotary pairs of a head: head_dim <= 256
+constexpr long long kFillWarps = 148 * 32;
 
 struct NrParams {
   AppendArgs A;
@@ -35,252 +41,344 @@ struct NrParams {
   const int32_t *pos;  // null: positions from P
   int n_tok, Hq, Hkv, d, di;
   int rot, rot_i;
-  float eps, w_off;
+  int parts;           // warps per token
+  int sh_d, sh_i;      // log2 of the lanes of a head of d (di) elements
+  int nq, nk, n_rows;  // a token's warp rows of q, of k, of everything
+  float eps, w_off, inv_d;
   const void *qw, *kw;
   int *status;
   // theta^(-2i/rot) / 2 pi as fractions of a turn, times 2^64
   uint64_t freq[kMaxHalf], freq_i[kMaxHalf];
 };
 
-template <typename T> struct Raw8 { uint4 w[sizeof(T) / 2]; };
+// Two groups of four elements as they are stored.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> { uint2 a, b; };
+template <> struct Raw<float> { uint4 a, b; };
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T *p) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = ((const uint4 *)p)[i];
-  return r;
+__device__ __forceinline__ void load_raw(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *p, const __nv_bfloat16 *q) {
+  r.a = *(const uint2 *)p;
+  r.b = *(const uint2 *)q;
 }
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const Raw8<T> &r) {
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) ((uint4 *)p)[i] = r.w[i];
+__device__ __forceinline__ void load_raw(Raw<float> &r, const float *p, const float *q) {
+  r.a = *(const uint4 *)p;
+  r.b = *(const uint4 *)q;
 }
-__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16> &r, float (&x)[8]) {
-  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void store_raw(const Raw<__nv_bfloat16> &r, __nv_bfloat16 *p, __nv_bfloat16 *q) {
+  *(uint2 *)p = r.a;
+  *(uint2 *)q = r.b;
 }
-__device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[4 * i] = __uint_as_float(r.w[i].x);
-    x[4 * i + 1] = __uint_as_float(r.w[i].y);
-    x[4 * i + 2] = __uint_as_float(r.w[i].z);
-    x[4 * i + 3] = __uint_as_float(r.w[i].w);
-  }
+__device__ __forceinline__ void store_raw(const Raw<float> &r, float *p, float *q) {
+  *(uint4 *)p = r.a;
+  *(uint4 *)q = r.b;
 }
-__device__ __forceinline__ void pack8(Raw8<__nv_bfloat16> &r, const float (&x)[8]) {
-  r.w[0] = make_uint4(sm100::pack_bf16x2(x[0], x[1]), sm100::pack_bf16x2(x[2], x[3]),
-                      sm100::pack_bf16x2(x[4], x[5]), sm100::pack_bf16x2(x[6], x[7]));
+// Four elements as two packed pairs of fp32, and back with one rounding.
+__device__ __forceinline__ void unpack(const uint2 &r, uint64_t (&x)[2]) {
+  x[0] = sm100::f2_pack(r.x << 16, r.x & 0xffff0000u);
+  x[1] = sm100::f2_pack(r.y << 16, r.y & 0xffff0000u);
 }
-__device__ __forceinline__ void pack8(Raw8<float> &r, const float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    r.w[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]),
-                        __float_as_uint(x[4 * i + 3]));
+__device__ __forceinline__ void unpack(const uint4 &r, uint64_t (&x)[2]) {
+  x[0] = sm100::f2_pack(r.x, r.y);
+  x[1] = sm100::f2_pack(r.z, r.w);
 }
-template <typename T>
-__device__ __forceinline__ Raw8<T> shfl8(const Raw8<T> &r, int src) {
-  Raw8<T> o;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
-    o.w[i].x = __shfl_sync(0xffffffffu, r.w[i].x, src);
-    o.w[i].y = __shfl_sync(0xffffffffu, r.w[i].y, src);
-    o.w[i].z = __shfl_sync(0xffffffffu, r.w[i].z, src);
-    o.w[i].w = __shfl_sync(0xffffffffu, r.w[i].w, src);
-  }
-  return o;
+__device__ __forceinline__ void pack(uint2 &r, const uint64_t (&x)[2]) {
+  float a, b;
+  sm100::f2_unpack(x[0], a, b);
+  r.x = sm100::pack_bf16x2(a, b);
+  sm100::f2_unpack(x[1], a, b);
+  r.y = sm100::pack_bf16x2(a, b);
 }
-
-// lanes a head of dim elements takes: a power of two, 8 elements a lane
-__device__ __forceinline__ int head_lanes(int dim) {
-  int w = 1;
-  while (w * 8 < dim) w <<= 1;
-  return w;
+__device__ __forceinline__ void pack(uint4 &r, const uint64_t (&x)[2]) {
+  float a, b;
+  sm100::f2_unpack(x[0], a, b);
+  r.x = __float_as_uint(a);
+  r.y = __float_as_uint(b);
+  sm100::f2_unpack(x[1], a, b);
+  r.z = __float_as_uint(a);
+  r.w = __float_as_uint(b);
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 enum { kSegQ = 0, kSegK = 1, kSegV = 2, kSegKi = 3 };
 
-// A lane's share of one warp row of the token's heads.
-struct Item {
-  int seg, head, j, lanes;  // lane j of the head's `lanes`
-  bool live;                // the lane holds elements of a head
+// Where a lane's elements are in a head: e0 .. e0 + 3 and e1 .. e1 + 3, rotation partners of each
+// other in the lanes of the head's first `rot` elements.
+struct Place {
+  int lanes, j, e0, e1;
+  bool live, turns;
+};
+__device__ __forceinline__ Place place_of(int dim, int shift, int rot, int lane) {
+  Place p;
+  p.lanes = 1 << shift;
+  p.j = lane & (p.lanes - 1);
+  p.live = p.j * 8 < dim;
+  const int pairs = rot >> 3;  // lanes that rotate
+  p.turns = p.j < pairs;
+  p.e0 = p.turns ? 4 * p.j : 8 * p.j;
+  p.e1 = p.turns ? p.e0 + (rot >> 1) : p.e0 + 4;
+  return p;
+}
+
+// Cosine and sine of 2 pi turn / 2^32: the nearest quarter turn q and the rest x in
+// [-pi/4, pi/4], whose Taylor sums to x^8 and x^9 are within 2^-25; a quarter turn swaps the
+// two and moves a sign.
+__device__ __forceinline__ void turn_cos_sin(uint32_t turn, float &c, float &s) {
+  const uint32_t q = (turn + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(turn - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float y = x * x;
+  float a = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  a = fmaf(a, y, 1.f / 120.f);
+  a = fmaf(a, y, -1.f / 6.f);
+  a = fmaf(a * y, x, x);
+  float b = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
+  b = fmaf(b, y, 1.f / 24.f);
+  b = fmaf(b, y, -0.5f);
+  b = fmaf(b, y, 1.f);
+  const float u = q & 1 ? a : b, v = q & 1 ? b : a;
+  c = (q + 1) & 2 ? -u : u;
+  s = q & 2 ? -v : v;
+}
+
+// out0 = x0 a0 + x1 b0, out1 = x1 a1 + x0 b1 (times the norm)
+struct Coef {
+  uint64_t a0[2], b0[2], a1[2], b1[2];
 };
 
+// A lane's share of some of a token's warp rows of one kind of head: `rows` of them from src to dst,
+// `step` elements apart.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_norm_rope(const __grid_constant__ NrParams P) {
-  __shared__ float s_cos[2 * kMaxHalf], s_sin[2 * kMaxHalf];  // q/k angles, then the indexer's
-  __shared__ int s_seq[4];                                    // sequence (-1: none), position, length
-  const int n = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const AppendArgs &A = P.A;
-
-  const int wd = head_lanes(P.d), wi = head_lanes(P.di);
-  const int per_d = 32 / wd;  // heads of d elements per warp row
-  const int nq = A.q ? (P.Hq + per_d - 1) / per_d : 0;
-  const int nk = A.k ? (P.Hkv + per_d - 1) / per_d : 0;
-  const int nv = A.v ? nk : 0;
-  const int n_items = nq + nk + nv + (A.ki ? 1 : 0);
-
-  auto item = [&](int i) {
-    Item it;
-    it.live = i < n_items;
-    int first = 0, heads = P.Hq, dim = P.d;
-    it.seg = kSegQ;
-    if (i >= nq + nk + nv) it.seg = kSegKi, first = nq + nk + nv, heads = 1, dim = P.di;
-    else if (i >= nq + nk) it.seg = kSegV, first = nq + nk, heads = P.Hkv;
-    else if (i >= nq) it.seg = kSegK, first = nq, heads = P.Hkv;
-    it.lanes = it.seg == kSegKi ? wi : wd;
-    it.j = lane & (it.lanes - 1);
-    it.head = (i - first) * (32 / it.lanes) + lane / it.lanes;
-    it.live = it.live && it.head < heads && it.j * 8 < dim;
-    return it;
-  };
-  auto source = [&](const Item &it) {
-    const long long row = it.seg == kSegQ ? A.q_row : it.seg == kSegK ? A.k_row : it.seg == kSegV ? A.v_row : A.ki_row;
-    const void *base = it.seg == kSegQ ? A.q : it.seg == kSegK ? A.k : it.seg == kSegV ? A.v : A.ki;
-    return (const T *)base + (long long)n * row + it.head * P.d + it.j * 8;
-  };
-
-  // the first rows' loads go out before the position is known
-  Item items[kBatch];
-  Raw8<T> raw[kBatch];
+struct Rows {
+  const T *src;
+  T *dst;
+  long long src_step, dst_step;
+  int rows;
+  int live;  // rows in which this lane holds elements
+};
+template <typename T>
+__device__ __forceinline__ void load_rows(const Rows<T> &w, const Place &p, int r, Raw<T> (&raw)[kBatch]) {
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    items[u] = item(warp + u * kWarps);
-    raw[u] = Raw8<T>{};
-    if (items[u].live) raw[u] = load8(source(items[u]));
+    raw[u] = Raw<T>{};
+    if (r + u < w.live) load_raw(raw[u], w.src + (r + u) * w.src_step, w.src + (r + u) * w.src_step + (p.e1 - p.e0));
+  }
+}
+// kCopy: as they are. The first batch is in raw already. kLanes: lanes of a head, 0 if only p knows.
+template <typename T, int kLanes, bool kCopy>
+__device__ __forceinline__ void run_rows(const Rows<T> &w, const Place &p, const Coef &c, bool normed, float inv_d, float eps,
+                                         Raw<T> (&raw)[kBatch]) {
+  using namespace sm100;
+  const bool all_turn = __all_sync(0xffffffffu, p.turns);
+  for (int r = 0; r < w.rows; r += kBatch) {
+    if (r) load_rows(w, p, r, raw);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (r + u >= w.rows) break;  // the same for the whole warp
+      if (!kCopy) {
+        uint64_t x0[2], x1[2], y0[2], y1[2];
+        unpack(raw[u].a, x0);
+        unpack(raw[u].b, x1);
+        if (normed) {
+          const uint64_t q = f2_add(f2_fma(x0[0], x0[0], f2_mul(x0[1], x0[1])), f2_fma(x1[0], x1[0], f2_mul(x1[1], x1[1])));
+          float sa, sb;
+          f2_unpack(q, sa, sb);
+          float ss = sa + sb;
+          if (kLanes) {
+#pragma unroll
+            for (int o = kLanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          } else {
+            for (int o = p.lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          }
+          const uint64_t rr = f2_splat(rsqrtf(fmaf(ss, inv_d, eps)));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x0[e] = f2_mul(x0[e], rr);
+            x1[e] = f2_mul(x1[e], rr);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // elements that do not rotate take nothing from their neighbours, infinities least of all
+          y0[e] = f2_mul(x0[e], c.a0[e]);
+          y1[e] = f2_mul(x1[e], c.a1[e]);
+          if (all_turn || p.turns) {
+            y0[e] = f2_fma(x1[e], c.b0[e], y0[e]);
+            y1[e] = f2_fma(x0[e], c.b1[e], y1[e]);
+          }
+        }
+        pack(raw[u].a, y0);
+        pack(raw[u].b, y1);
+      }
+      if (r + u < w.live) store_raw(raw[u], w.dst + (r + u) * w.dst_step, w.dst + (r + u) * w.dst_step + (p.e1 - p.e0));
+    }
+  }
+}
+
+// kD: the head dim, 0 for one without an instantiation of its own
+template <typename T, bool kPaged, int kD>
+__global__ void __launch_bounds__(kWarps * 32) k_norm_rope(const __grid_constant__ NrParams P) {
+  using namespace sm100;
+  const int lane = threadIdx.x & 31;
+  // warp `part` of token n
+  const unsigned g = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int n = P.parts == 1 ? (int)g : (int)(g / (unsigned)P.parts), part = P.parts == 1 ? 0 : (int)(g % (unsigned)P.parts);
+  if (n >= P.n_tok) return;
+  const AppendArgs &A = P.A;
+
+  // warp rows: those of q, then k, v and the indexer key
+  constexpr int kLanes = kD / 8;
+  const int d = kD ? kD : P.d, sh_d = kD == 64 ? 3 : kD == 128 ? 4 : kD == 256 ? 5 : P.sh_d;
+  const Place pd = place_of(d, sh_d, P.rot, lane);
+  const int sh = 5 - sh_d, per = 1 << sh, sub = lane >> sh_d;  // heads per warp row, the lane's among them
+  const int f1 = P.nq, f2 = P.nq + P.nk, f3 = P.nq + (kPaged ? 2 : 1) * P.nk;  // first rows of k, v and ki
+  const int i_begin = P.parts == 1 ? 0 : part * P.n_rows / P.parts;
+  const int i_end = P.parts == 1 ? P.n_rows : (part + 1) * P.n_rows / P.parts;
+  auto first_of = [&](int seg) { return seg == kSegQ ? 0 : seg == kSegK ? f1 : seg == kSegV ? f2 : f3; };
+
+  // this warp's rows of one kind, without their destination
+  auto rows_of = [&](int seg) {
+    Rows<T> w;
+    const int f = first_of(seg), lo = max(i_begin - f, 0), hi = min(i_end, seg == kSegKi ? P.n_rows : first_of(seg + 1)) - f;
+    const T *base = seg == kSegQ ? (const T *)A.q + (long long)n * A.q_row
+                    : seg == kSegK ? (const T *)A.k + (long long)n * A.k_row
+                                   : (const T *)A.v + (long long)n * A.v_row;
+    w.rows = max(hi - lo, 0);
+    w.src_step = d << sh;
+    w.src = base + ((lo << sh) + sub) * d + pd.e0;
+    // the lane's head in row r is (lo + r) per + sub
+    const int heads = (seg == kSegQ ? P.Hq : P.Hkv) - (lo << sh) - sub;
+    w.live = pd.live ? min(w.rows, (heads + per - 1) >> sh) : 0;
+    w.dst = nullptr;
+    w.dst_step = 0;
+    return w;
+  };
+  Place pi = pd;
+  Rows<T> wi;  // the indexer key's row
+  if (kPaged && A.ki) {
+    pi = place_of(P.di, P.sh_i, P.rot_i, lane);
+    wi.rows = max(i_end - max(i_begin, f3), 0);
+    wi.src_step = 0;
+    wi.src = (const T *)A.ki + (long long)n * A.ki_row + pi.e0;
+    wi.live = pi.live && lane == pi.j ? wi.rows : 0;
+  } else {
+    wi.rows = 0;
   }
 
-  int b = 0, t = 0, len = 0;
-  if (P.pos) {
+  // the first rows' loads go out before the position is known
+  Raw<T> raw[kBatch];
+  const int seg0 = i_begin < f1 ? kSegQ : i_begin < f2 ? kSegK : i_begin < f3 ? kSegV : kSegKi;
+  if (!kPaged || seg0 != kSegKi) load_rows(rows_of(seg0), pd, 0, raw);
+  else load_rows(wi, pi, 0, raw);
+
+  int b = 0, t = 0, len = 0, page = 0;
+  bool page_ok = true;
+  if (!kPaged) {
     t = P.pos[n];
   } else {
     // the row's sequence: the last b with q_start[b] <= n, by a 32-way search
-    if (warp == 0) {
-      int lo = 0, hi = P.P.batch;  // q_start[lo] <= n (if any), q_start[hi] > n
-      if (P.P.q_start[0] > n || P.P.q_start[hi] <= n) {
-        lo = -1;
-      } else {
-        while (hi - lo > 1) {
-          const int step = (hi - lo + 31) / 32;
-          const int at = lo + step * (lane + 1);
-          const unsigned le = __ballot_sync(0xffffffffu, at < hi && P.P.q_start[at] <= n);
-          const int c = __popc(le);
-          hi = min(hi, lo + step * (c + 1));
-          lo += step * c;
-        }
-      }
-      int pos = -1, ln = 0;
-      if (lo >= 0) {
-        const PagedSeq s = paged_seq(P.P, lo, lane == 0 ? P.status : nullptr);
-        if (s.ok && n >= s.q0 && n < s.q0 + s.n) {
-          pos = s.len - s.n + (n - s.q0);
-          ln = s.len;
-        }
-      }
-      if (lane == 0) {
-        s_seq[0] = pos >= 0 ? lo : -1;
-        s_seq[1] = pos;
-        s_seq[2] = ln;
-      }
+    int lo = 0, hi = P.P.batch;
+    if (P.P.q_start[0] > n || P.P.q_start[hi] <= n) return;  // a row of no sequence
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + step * (lane + 1);
+      const int c = __popc(__ballot_sync(0xffffffffu, at < hi && P.P.q_start[at] <= n));
+      hi = min(hi, lo + step * (c + 1));
+      lo += step * c;
     }
-    __syncthreads();
-    b = s_seq[0];
-    t = s_seq[1];
-    len = s_seq[2];
-    if (b < 0) return;  // a row of no sequence
-  }
-  for (int i = threadIdx.x; i < 2 * kMaxHalf; i += kWarps * 32) {
-    const bool own = i < kMaxHalf;
-    const int e = own ? i : i - kMaxHalf;
-    if (2 * e < (own ? P.rot : A.ki ? P.rot_i : 0)) {
-      // position times the frequency, modulo a turn; the signed upper half is the phase
-      const uint64_t turn = (own ? P.freq[e] : P.freq_i[e]) * (uint64_t)(int64_t)t;
-      const float half_turns = (float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(half_turns, &s_sin[i], &s_cos[i]);
-    }
-  }
-  __syncthreads();
-
-  // where the token's rows of the cache go
-  int page = 0;
-  bool page_ok = true;
-  if (!P.pos) {
+    const PagedSeq s = paged_seq(P.P, lo, lane == 0 ? P.status : nullptr);
+    if (!s.ok || n < s.q0 || n >= s.q0 + s.n) return;
+    b = lo;
+    t = s.len - s.n + (n - s.q0);
+    len = s.len;
     page = P.P.table[(size_t)b * P.P.max_pages + (t >> P.P.ps_shift)];
     page_ok = page >= 0 && page < P.P.n_pages;
-    if (!page_ok && threadIdx.x == 0) record_status(P.status, QSA_ERR_DEVICE_CHECK);
-    if (A.ki && len > A.ki_cap && threadIdx.x == 0) record_status(P.status, QSA_ERR_DEVICE_CHECK);
+    if (lane == 0 && (!page_ok || (A.ki && len > A.ki_cap))) record_status(P.status, QSA_ERR_DEVICE_CHECK);
   }
 
-  for (int i0 = warp; i0 < n_items; i0 += kBatch * kWarps) {
-    if (i0 != warp) {
+  // cosine and sine of the lane's four pairs
+  auto angles = [&](const uint64_t *freq, int j, uint64_t (&c)[2], uint64_t (&s)[2]) {
+    float cs[4], sn[4];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        items[u] = item(i0 + u * kWarps);
-        raw[u] = Raw8<T>{};
-        if (items[u].live) raw[u] = load8(source(items[u]));
+    for (int e = 0; e < 4; ++e) {
+      // position times frequency, modulo a turn, in 2^-32 turns
+      const uint32_t turn = (uint32_t)((freq[4 * j + e] * (uint64_t)(int64_t)t) >> 32);
+      turn_cos_sin(turn, cs[e], sn[e]);
+    }
+    c[0] = f2_pack(__float_as_uint(cs[0]), __float_as_uint(cs[1]));
+    c[1] = f2_pack(__float_as_uint(cs[2]), __float_as_uint(cs[3]));
+    s[0] = f2_pack(__float_as_uint(sn[0]), __float_as_uint(sn[1]));
+    s[1] = f2_pack(__float_as_uint(sn[2]), __float_as_uint(sn[3]));
+  };
+  const uint64_t one = f2_splat(1.f), minus = f2_splat(-1.f);
+  uint64_t c[2] = {one, one}, s[2] = {0, 0};
+  if (pd.turns && i_begin < f2) angles(P.freq, pd.j, c, s);
+  auto coef_of = [&](const T *w) {
+    uint64_t w0[2] = {one, one}, w1[2] = {one, one};
+    if (w && pd.live) {
+      Raw<T> rw;
+      load_raw(rw, w + pd.e0, w + pd.e1);
+      unpack(rw.a, w0);
+      unpack(rw.b, w1);
+      const uint64_t off = f2_splat(P.w_off);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        w0[e] = f2_add(w0[e], off);
+        w1[e] = f2_add(w1[e], off);
       }
     }
+    Coef k;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (i0 + u * kWarps >= n_items) continue;  // the same for the whole warp
-      const Item it = items[u];
-      const bool qk = it.seg == kSegQ || it.seg == kSegK;
-      const T *w = qk ? (const T *)(it.seg == kSegQ ? P.qw : P.kw) : nullptr;
-      const int rot = qk ? P.rot : it.seg == kSegKi ? P.rot_i : 0;
-      Raw8<T> out = raw[u];
-      if (w || rot) {
-        float x[8], y[8];
-        unpack8(raw[u], x);
-        const int e0 = it.j * 8, half = rot >> 1;
-        const bool turns = e0 < rot, lower = e0 < half;
-        const int mate = turns ? (lower ? e0 + half : e0 - half) : e0;  // first element of the partner lane
-        const Raw8<T> other = shfl8(raw[u], (lane & ~(it.lanes - 1)) + (mate >> 3));
-        unpack8(other, y);
-        if (w) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          for (int o = it.lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss / (float)P.d + P.eps);
-          if (it.live) {
-            float wx[8], wy[8];
-            unpack8(load8(w + e0), wx);
-            unpack8(load8(w + mate), wy);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = x[e] * r * (wx[e] + P.w_off);
-              y[e] = y[e] * r * (wy[e] + P.w_off);
-            }
-          }
-        }
-        if (turns) {
-          const int a = (it.seg == kSegKi ? kMaxHalf : 0) + (lower ? e0 : e0 - half);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e], lower ? -s_sin[a + e] : s_sin[a + e], x[e] * s_cos[a + e]);
-        }
-        pack8(out, x);
-      }
-      if (!it.live) continue;
-      T *dst;
-      if (it.seg == kSegQ) {
-        dst = (T *)A.q_out + (long long)n * A.q_out_row + it.head * P.d;
-      } else if (it.seg == kSegKi) {
-        if (len > A.ki_cap) continue;
-        dst = (T *)A.ki_cache + ((size_t)b * A.ki_cap + t) * P.di;
-      } else if (P.pos) {
-        dst = (T *)A.k_out + (long long)n * A.k_out_row + it.head * P.d;
-      } else {
-        if (!page_ok) continue;
-        dst = (T *)(it.seg == kSegK ? A.k_pages : A.v_pages) +
-              ((((size_t)page * P.Hkv + it.head) << P.P.ps_shift) + (t & (P.P.ps - 1))) * P.d;
-      }
-      store8(dst + it.j * 8, out);
+    for (int e = 0; e < 2; ++e) {
+      k.a0[e] = f2_mul(w0[e], c[e]);
+      k.b0[e] = f2_mul(f2_mul(w1[e], s[e]), minus);
+      k.a1[e] = f2_mul(w1[e], c[e]);
+      k.b1[e] = f2_mul(w0[e], s[e]);
     }
+    return k;
+  };
+
+  const long long slot = kPaged ? (((long long)page * P.Hkv) << P.P.ps_shift) + (t & (P.P.ps - 1)) : 0;
+#pragma unroll
+  for (int seg = kSegQ; seg <= (kPaged ? kSegV : kSegK); ++seg) {
+    Rows<T> w = rows_of(seg);
+    if (w.rows == 0) continue;
+    const int head = (max(i_begin - first_of(seg), 0) << sh) + sub;  // the lane's in the first row
+    if (seg == kSegQ || !kPaged) {
+      w.dst = seg == kSegQ ? (T *)A.q_out + (long long)n * A.q_out_row : (T *)A.k_out + (long long)n * A.k_out_row;
+      w.dst += head * d + pd.e0;
+      w.dst_step = d << sh;
+    } else {
+      w.dst = (T *)(seg == kSegK ? A.k_pages : A.v_pages) + (slot + ((long long)head << P.P.ps_shift)) * d + pd.e0;
+      w.dst_step = ((long long)d << P.P.ps_shift) << sh;
+      if (!page_ok) w.live = 0;
+    }
+    if (seg != seg0) load_rows(w, pd, 0, raw);
+    const T *weight = (const T *)(seg == kSegQ ? P.qw : P.kw);
+    if (seg == kSegV || (!weight && P.rot == 0)) {
+      run_rows<T, kLanes, true>(w, pd, Coef{}, false, 0.f, 0.f, raw);
+    } else {
+      run_rows<T, kLanes, false>(w, pd, coef_of(weight), weight != nullptr, P.inv_d, P.eps, raw);
+    }
+  }
+  if (kPaged && wi.rows) {
+    if (len > A.ki_cap) wi.live = 0;
+    wi.dst = (T *)A.ki_cache + ((size_t)b * A.ki_cap + t) * P.di + pi.e0;
+    wi.dst_step = 0;
+    if (seg0 != kSegKi) load_rows(wi, pi, 0, raw);
+    Coef k;
+    uint64_t ci[2] = {one, one}, si[2] = {0, 0};
+    if (pi.turns) angles(P.freq_i, pi.j, ci, si);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      k.a0[e] = k.a1[e] = ci[e];
+      k.b0[e] = f2_mul(si[e], minus);
+      k.b1[e] = si[e];
+    }
+    if (P.rot_i == 0) run_rows<T, 0, true>(wi, pi, k, false, 0.f, 0.f, raw);
+    else run_rows<T, 0, false>(wi, pi, k, false, 0.f, 0.f, raw);
   }
 }
 
@@ -302,13 +400,34 @@ cudaError_t launch(const Dims &D, const NormRope &N, NrParams &P, cudaStream_t s
   P.rot_i = N.rot_i;
   P.eps = N.eps;
   P.w_off = N.w_off;
+  P.inv_d = 1.f / (float)D.d;
   P.qw = N.qw;
   P.kw = N.kw;
   frequencies(P.freq, N.rot, N.log2_theta);
   frequencies(P.freq_i, N.rot_i, N.log2_theta);
+  // With few tokens a token's rows are spread over more warps, down to one row a warp, until
+  // there is a warp for each of about 32 per SM.
+  P.sh_d = P.sh_i = 0;
+  while ((8 << P.sh_d) < D.d) ++P.sh_d;
+  while ((8 << P.sh_i) < D.di) ++P.sh_i;
+  const int per = 32 >> P.sh_d;
+  P.nq = P.A.q ? (D.Hq + per - 1) / per : 0;
+  P.nk = P.A.k ? (D.Hkv + per - 1) / per : 0;
+  P.n_rows = P.nq + P.nk * (P.pos ? 1 : 2) + (P.A.ki ? 1 : 0);
+  P.parts = (int)std::max(1LL, std::min((long long)P.n_rows, kFillWarps / P.n_tok));
+  const long long blocks = ((long long)P.n_tok * P.parts + kWarps - 1) / kWarps;
+  if (blocks * kWarps > 0xffffffffLL) return cudaErrorNotSupported;
   note_launch();
-  if (D.bf16) k_norm_rope<__nv_bfloat16><<<P.n_tok, kWarps * 32, 0, st>>>(P);
-  else k_norm_rope<float><<<P.n_tok, kWarps * 32, 0, st>>>(P);
+  auto pick = [&](auto d) {
+    constexpr int kD = decltype(d)::value;
+    return D.bf16 ? (P.pos ? k_norm_rope<__nv_bfloat16, false, kD> : k_norm_rope<__nv_bfloat16, true, kD>)
+                  : (P.pos ? k_norm_rope<float, false, kD> : k_norm_rope<float, true, kD>);
+  };
+  auto kern = D.d == 64    ? pick(std::integral_constant<int, 64>{})
+              : D.d == 128 ? pick(std::integral_constant<int, 128>{})
+              : D.d == 256 ? pick(std::integral_constant<int, 256>{})
+                           : pick(std::integral_constant<int, 0>{});
+  kern<<<(unsigned)blocks, kWarps * 32, 0, st>>>(P);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) note_error("k_norm_rope launch", e);
   return e;

@@ -400,6 +400,10 @@ class NormRope:
     def __init__(self, q_weight, k_weight, eps: float, weight_offset: float, rope_theta: float, rotary_dim: int,
                  indexer_rotary_dim: int):
         self.q_weight, self.k_weight = q_weight, k_weight
+        kinds = [(w.dtype, w.shape) for w in (q_weight, k_weight) if w is not None]
+        if kinds and kinds[0] != kinds[-1]:
+            raise ValueError(f"q_weight and k_weight differ: {kinds[0]} and {kinds[-1]}")
+        self.kind = kinds[0] if kinds else None  # dtype and shape, checked against the config in every call
         self.c = qsa_norm_rope_t(eps, weight_offset, rope_theta, rotary_dim, indexer_rotary_dim, _p(q_weight),
                                  _p(k_weight))
 
@@ -446,48 +450,60 @@ def alloc_paged_workspace(cfg, pg: PagedBatch, device=None) -> torch.Tensor:
 
 def _rows(t: torch.Tensor, dtype: torch.dtype, shape, name: str):
     """(address, row stride) of packed rows: everything behind the first axis is dense."""
-    _want(t, dtype, shape, name)
+    if t.dtype != dtype or t.shape != shape:
+        _want(t, dtype, shape, name)
     if not t.is_cuda:
         raise ValueError("QSA tensors must live on a CUDA device")
-    want = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if st != want and n != 1:
+    st, dense = t.stride(), 1
+    for n, stride in zip(shape[:0:-1], st[:0:-1]):
+        if stride != dense and n != 1:
             raise ValueError(f"{name}: a row's heads must be dense")
-        want *= n
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), want)
+        dense *= n
+    return t.data_ptr(), st[0] if shape[0] > 1 else dense
 
 
-def _same_device(first: torch.Tensor, *others):
-    """The call runs on the current device: every tensor has to be there."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+def _plain(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
+    """Address of a dense tensor of that type and shape."""
+    if t.dtype != dtype or t.shape != shape:
+        _want(t, dtype, shape, name)
+    return _p(t)
+
+
+def _here(first: torch.Tensor, *others) -> int:
+    """The call runs on the current device: every tensor has to be there. Returns its index."""
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _norm_weights(cfg, nr: NormRope):
+    if nr.kind is not None and nr.kind != (_elem(cfg), (cfg.head_dim,)):
+        raise ValueError(f"norm weights: {nr.kind[0]} {tuple(nr.kind[1])}, expected {_elem(cfg)} {(cfg.head_dim,)}")
 
 
 def qsa_norm_rope(cfg, nr: NormRope, pos, q, k, q_out, k_out, stream=None):
     """RMS norm and rotation of q [n][Hq][d] and k [n][Hkv][d] (rows may be strided) at pos [n] into
     q_out / k_out, which may be q / k themselves. q and q_out, or k and k_out, may be None."""
-    dt, n = _elem(cfg), pos.shape[0]
-    _want(pos, torch.int32, (n,), "pos")
-    a = [None, 0, None, 0, None, 0, None, 0]
+    dt, n, d = _elem(cfg), pos.shape[0], cfg.head_dim
+    qa = ka = qo = ko = (None, 0)
     if q is not None:
-        shape = (n, cfg.num_attention_heads, cfg.head_dim)
-        a[0:2], a[2:4] = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
+        shape = (n, cfg.num_attention_heads, d)
+        qa, qo = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
     if k is not None:
-        shape = (n, cfg.num_key_value_heads, cfg.head_dim)
-        a[4:6], a[6:8] = _rows(k, dt, shape, "k"), _rows(k_out, dt, shape, "k_out")
+        shape = (n, cfg.num_key_value_heads, d)
+        ka, ko = _rows(k, dt, shape, "k"), _rows(k_out, dt, shape, "k_out")
     _norm_weights(cfg, nr)
-    _same_device(pos, q, k, q_out, k_out, nr.q_weight, nr.k_weight)
-    _check(_lib.qsa_norm_rope(ctypes.byref(cfg), ctypes.byref(nr.c), _p(pos), n, *a, _stream(stream)), "qsa_norm_rope")
-
-
-def _norm_weights(cfg, nr: NormRope):
-    for name, w in (("q_weight", nr.q_weight), ("k_weight", nr.k_weight)):
-        if w is not None:
-            _want(w, _elem(cfg), (cfg.head_dim,), name)
+    dev = _here(pos, q, k, q_out, k_out, nr.q_weight, nr.k_weight)
+    _check(_lib.qsa_norm_rope(ctypes.byref(cfg), ctypes.byref(nr.c), _plain(pos, torch.int32, (n,), "pos"), n, *qa, *qo,
+                              *ka, *ko, _raw_stream(stream, dev)), "qsa_norm_rope")
 
 
 def qsa_paged_append(cfg, nr: Optional[NormRope], pg: PagedBatch, k, v, k_pages, v_pages, workspace, q=None, q_out=None,
@@ -496,42 +512,41 @@ def qsa_paged_append(cfg, nr: Optional[NormRope], pg: PagedBatch, k, v, k_pages,
     q [n_tok][Hq][d] into q_out and ki [n_tok][di] into ki_cache [batch][cap][di] beside them."""
     dt, n, Hkv, d = _elem(cfg), pg.n_tok, cfg.num_key_value_heads, cfg.head_dim
     pool = (pg.n_pages, Hkv, pg.page_size, d)
-    _want(k_pages, dt, pool, "k_pages")
-    _want(v_pages, dt, pool, "v_pages")
-    t = qsa_append_t()
-    t.k, t.k_row = _rows(k, dt, (n, Hkv, d), "k")
-    t.v, t.v_row = _rows(v, dt, (n, Hkv, d), "v")
-    t.k_pages, t.v_pages = _p(k_pages), _p(v_pages)
+    ka, va = _rows(k, dt, (n, Hkv, d), "k"), _rows(v, dt, (n, Hkv, d), "v")
+    qa = qo = kia = (None, 0)
+    ki_ptr, ki_cap = None, 0
     if q is not None:
         shape = (n, cfg.num_attention_heads, d)
-        t.q, t.q_row = _rows(q, dt, shape, "q")
-        t.q_out, t.q_out_row = _rows(q_out, dt, shape, "q_out")
+        qa, qo = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
     if ki is not None:
-        t.ki, t.ki_row = _rows(ki, dt, (n, cfg.indexer_head_dim), "ki")
-        _want(ki_cache, dt, (pg.c.batch, ki_cache.shape[1], cfg.indexer_head_dim), "ki_cache")
-        t.ki_cache, t.ki_cap = _p(ki_cache), ki_cache.shape[1]
+        di = cfg.indexer_head_dim
+        ki_cap = ki_cache.shape[1]
+        kia = _rows(ki, dt, (n, di), "ki")
+        ki_ptr = _plain(ki_cache, dt, (pg.c.batch, ki_cap, di), "ki_cache")
     if nr is not None:
         _norm_weights(cfg, nr)
-        _same_device(k, nr.q_weight, nr.k_weight)
-    _same_device(k, v, k_pages, v_pages, workspace, q, q_out, ki, ki_cache, pg.q_start, pg.kv_len, pg.page_table)
+        _here(k, nr.q_weight, nr.k_weight)
+    dev = _here(k, v, k_pages, v_pages, workspace, q, q_out, ki, ki_cache, pg.q_start, pg.kv_len, pg.page_table)
+    t = qsa_append_t(ka[0], va[0], ka[1], va[1], _plain(k_pages, dt, pool, "k_pages"), _plain(v_pages, dt, pool, "v_pages"),
+                     *qa, *qo, *kia, ki_ptr, ki_cap)
     _check(_lib.qsa_paged_append(ctypes.byref(cfg), ctypes.byref(nr.c) if nr is not None else None, ctypes.byref(pg.c),
-                                 ctypes.byref(t), _p(workspace), workspace.numel(), _stream(stream)), "qsa_paged_append")
+                                 ctypes.byref(t), _p(workspace), workspace.numel(), _raw_stream(stream, dev)),
+           "qsa_paged_append")
 
 
 def qsa_paged_attn(cfg, pg: PagedBatch, q, k_pages, v_pages, sel, out, workspace, stream=None):
     """Attention of the packed rows q [n_tok][Hq][d] over the pages [n_pages][Hkv][page_size][d], over every
     visible token (sel None) or the blocks in sel [n_tok][k] and the trailing range."""
     dt, n, d = _elem(cfg), pg.n_tok, cfg.head_dim
-    pool = (pg.n_pages, cfg.num_key_value_heads, pg.page_size, d)
-    _want(q, dt, (n, cfg.num_attention_heads, d), "q")
-    _want(out, dt, (n, cfg.num_attention_heads, d), "out")
-    _want(k_pages, dt, pool, "k_pages")
-    _want(v_pages, dt, pool, "v_pages")
+    pool, rows = (pg.n_pages, cfg.num_key_value_heads, pg.page_size, d), (n, cfg.num_attention_heads, d)
+    sel_ptr = None
     if sel is not None:
-        _want(sel, torch.int32, (n, qsa_topk_blocks(cfg)), "sel")
-    _same_device(q, k_pages, v_pages, sel, out, workspace, pg.q_start, pg.kv_len, pg.page_table)
-    _check(_lib.qsa_paged_attn(ctypes.byref(cfg), ctypes.byref(pg.c), _p(q), _p(k_pages), _p(v_pages), _p(sel), _p(out),
-                               _p(workspace), workspace.numel(), _stream(stream)), "qsa_paged_attn")
+        sel_ptr = _plain(sel, torch.int32, (n, qsa_topk_blocks(cfg)), "sel")
+    dev = _here(q, k_pages, v_pages, sel, out, workspace, pg.q_start, pg.kv_len, pg.page_table)
+    _check(_lib.qsa_paged_attn(ctypes.byref(cfg), ctypes.byref(pg.c), _plain(q, dt, rows, "q"),
+                               _plain(k_pages, dt, pool, "k_pages"), _plain(v_pages, dt, pool, "v_pages"), sel_ptr,
+                               _plain(out, dt, rows, "out"), _p(workspace), workspace.numel(), _raw_stream(stream, dev)),
+           "qsa_paged_attn")
 
 
 def qsa_selftest_wait_timeout(workspace, limit_ns: int = 50_000_000, stream=None):
