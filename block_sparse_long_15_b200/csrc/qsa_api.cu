@@ -537,7 +537,7 @@ qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRop
 constexpr int kChunkRows = 64;
 bool paged_chunks(const Dims &D, const Paged &G) { return D.bf16 && (long long)G.max_chunk * D.G >= kChunkRows; }
 size_t paged_scratch(const Dims &D, const Paged &G) {
-  return round256(paged_rows_workspace(D)) + (paged_chunks(D, G) ? round256(paged_tc_workspace()) : 0);
+  return round256(paged_rows_workspace(D)) + (paged_chunks(D, G) ? round256(paged_tc_workspace(D)) : 0);
 }
 
 // A packed tensor of rows of `width` elements, `row` elements apart.

@@ -1,0 +1,489 @@
+// What the chunk attention kernels over a paged cache share: the division of the work, the
+// warp that prepares it, and the merge of a unit's parts. A kernel's shape X has kD (head dim),
+// kTiles (128-row MMA tiles per unit) and kChunk (keys per chunk).
+//
+// Units differ in length and there may be fewer of them than SMs, so the keys that the units
+// see, laid end to end, are cut into C equal ranges, C = one per SM (fewer for little work),
+// and CTA c takes range c: no CTA waits for another, and at most the first and the last unit of
+// a range are shared with neighbours. A part of a unit leaves its unnormalised O with (m, l) per
+// row in the workspace, two slots per CTA, and k_paged_merge, one row a warp, joins them in order.
+#pragma once
+
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "qsa_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace qsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128;  // MMA M: (token, head) rows per tile
+constexpr int kHalf = 64;   // mask granularity: the smallest block size served
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMaxSeqs = 1024;  // sequences per launch
+constexpr int kMaxCtas = 152;
+constexpr int kMinKeys = 512;   // keys of a unit that make a CTA's range worth having
+constexpr int kBitWords = 2048;     // words of a segment's token bits
+constexpr int kBitTileWords = 128;  // and of its tiles' bits
+constexpr uint32_t kBitSlotBytes = (kBitWords + kBitTileWords) * 4;
+constexpr uint32_t kInfoBytes = 64;
+
+struct TcParams {
+  Dims D;
+  Paged P;
+  const int32_t *sel;  // null: every visible token
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  float *part_o;       // [2 C][rows of a unit][d] unnormalised O
+  float *part_ml;      // [2 C][rows of a unit][2]: m (log2 domain), l
+  int *status;
+  int T;               // tokens per tile
+  float sl2;           // scale * log2(e)
+  int C;               // CTAs
+  int b0, nb;          // sequences of this launch
+  int min_rows;        // sequences with fewer (token, head) rows are left to the row kernel
+  int box;             // keys per TMA box: min(page size, chunk)
+  int W;               // words a token's bits have in a segment
+};
+
+// ---------------------------------------------------------------- the key list
+// The list of all units' visible keys: sequence by sequence, KV head by KV head, unit by unit.
+// Unit u of a sequence with n new tokens of len sees w(u) = len - n + min(n, (u + 1) step) keys, step = tiles * T tokens.
+struct SeqPlan {
+  PagedSeq s;
+  int units;        // per KV head
+  long long keys;   // per KV head
+};
+template <class X>
+__device__ __forceinline__ SeqPlan seq_plan(const TcParams &P, int b, int *status) {
+  SeqPlan q;
+  q.s = paged_seq(P.P, P.b0 + b, status);
+  if ((long long)q.s.n * P.D.G < P.min_rows) q.s.n = 0;
+  const int step = X::kTiles * P.T;
+  q.units = (q.s.n + step - 1) / step;
+  q.keys = 0;
+  if (q.units) {
+    const long long u = q.units - 1;
+    q.keys = u * (q.s.len - q.s.n) + (long long)step * u * (u + 1) / 2 + q.s.len;
+  }
+  return q;
+}
+// Keys of the units before u (u < units) of one KV head.
+template <class X>
+__device__ __forceinline__ long long keys_before(const TcParams &P, const SeqPlan &q, long long u) {
+  return u * (q.s.len - q.s.n) + (long long)X::kTiles * P.T * u * (u + 1) / 2;
+}
+
+// pre[b]: keys of the sequences before b, in shared memory. Every thread of the block calls it.
+template <class X>
+__device__ void make_plan(const TcParams &P, long long *pre, int *status) {
+  __shared__ long long s_sum[32];
+  const int nt = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (P.nb + nt - 1) / nt;
+  const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
+  long long run = 0;
+  for (int b = a; b < z; ++b) {
+    run += seq_plan<X>(P, b, status).keys * P.D.Hkv;
+    pre[b + 1] = run;
+  }
+  long long incl = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  if (threadIdx.x == 0) pre[0] = 0;
+  __syncthreads();
+  long long before = incl - run;
+  for (int w = 0; w < warp; ++w) before += s_sum[w];
+  for (int b = a; b < z; ++b) pre[b + 1] += before;
+  __syncthreads();
+}
+__device__ __forceinline__ int ctas_of(const TcParams &P, long long total) {
+  return (int)min((long long)P.C, (total + kMinKeys - 1) / kMinKeys);
+}
+
+struct Unit {
+  int b, g, u;
+  long long first;  // its first key's place in the list
+  int w;            // keys it sees
+  SeqPlan q;
+};
+template <class X>
+__device__ __forceinline__ Unit unit_at(const TcParams &P, const long long *pre, long long x) {
+  Unit r;
+  int lo = 0, hi = P.nb;  // pre[lo] <= x < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  r.b = lo;
+  r.q = seq_plan<X>(P, lo, nullptr);
+  const long long in = x - pre[lo];
+  r.g = (int)(in / r.q.keys);
+  const long long y = in - r.g * r.q.keys;
+  int ul = 0, uh = r.q.units;
+  while (uh - ul > 1) {
+    const int mid = (ul + uh) >> 1;
+    if (keys_before<X>(P, r.q, mid) <= y) ul = mid;
+    else uh = mid;
+  }
+  r.u = ul;
+  r.first = pre[lo] + r.g * r.q.keys + keys_before<X>(P, r.q, ul);
+  r.w = r.q.s.len - r.q.s.n + min(r.q.s.n, (ul + 1) * X::kTiles * P.T);
+  return r;
+}
+// Where CTA c's range begins: c / C of the list, moved up to the next chunk of its unit (or to
+// the unit's end).
+template <class X>
+__device__ __forceinline__ long long range_start(const TcParams &P, const long long *pre, long long total, int C, int c) {
+  if (c >= C) return total;
+  const long long x = (long long)c * total / C;
+  const Unit r = unit_at<X>(P, pre, x);
+  const long long y = (x - r.first + X::kChunk - 1) / X::kChunk * X::kChunk;
+  return r.first + min(y, (long long)r.w);
+}
+// The CTA whose range holds place x (a chunk's beginning): floor(c T / C) <= x < floor((c + 1) T / C).
+__device__ __forceinline__ int cta_of(long long x, int C, long long total) {
+  return (int)(((x + 1) * C + total - 1) / total) - 1;
+}
+
+// A segment as the builder hands it to the other warps.
+struct UnitInfo {
+  int live;  // 0: no segment left
+  int b, g, q0, r0, n, len;
+  int slot;  // partial slot, -1: the whole unit
+  int ca, cb;     // chunks [ca, cb)
+  int cend[2];    // without a selection tile w sees the chunks below cend[w]
+  int part;       // bit 0: the first of the unit's segments here, bit 1: the last
+};
+static_assert(sizeof(UnitInfo) <= kInfoBytes, "unit info area");
+
+// Where the builder works in shared memory: two slots of everything.
+struct SlotArea {
+  uint64_t *full, *free;  // barriers [slot]
+  uint8_t *info;          // [slot] kInfoBytes
+  uint8_t *bits;          // [slot] kBitSlotBytes: token bits, then tile bits; with a selection
+  volatile int *abort_flag;
+};
+
+// The chunks of a segment: of the unit (the union of its tiles') and of each tile. With a
+// selection bit H i + h of a bit list stands for 64 keys: part h of the H in chunk ca + i.
+template <class X, bool kSel>
+struct Chunks {
+  static constexpr int H = X::kChunk / kHalf, kPer = 32 / H;  // chunks per word
+  const uint32_t *bits;  // a tile's nw words after the other's
+  int nw, ca, cend[2];
+  __device__ __forceinline__ Chunks(const UnitInfo &I, const uint32_t *tile_bits, int W)
+      : bits(tile_bits), nw(W), ca(I.ca), cend{I.cend[0], I.cend[1]} {}
+  __device__ __forceinline__ uint32_t word(int w) const { return X::kTiles == 2 ? bits[w] | bits[nw + w] : bits[w]; }
+  // Smallest chunk >= c of the unit, or -1.
+  __device__ __forceinline__ int next(int c) const {
+    if (!kSel) return c < (X::kTiles == 2 ? max(cend[0], cend[1]) : cend[0]) ? c : -1;
+    int w = (c - ca) / kPer;
+    if (w >= nw) return -1;
+    uint32_t x = word(w) & (0xffffffffu << (H * ((c - ca) % kPer)));
+    while (true) {
+      if (x) return ca + w * kPer + (__ffs(x) - 1) / H;
+      if (++w >= nw) return -1;
+      x = word(w);
+    }
+  }
+  __device__ __forceinline__ bool has(int w, int c) const {
+    return kSel ? (bits[w * nw + (c - ca) / kPer] >> (H * ((c - ca) % kPer))) & ((1u << H) - 1u) : c < cend[w];
+  }
+};
+
+// A wait taken by a whole warp: the same answer on every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
+}
+// A wait off the critical path that sleeps between polls.
+__device__ __forceinline__ bool idle_wait_warp(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  bool ok = true;
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      ok = false;
+      break;
+    }
+    __nanosleep(128);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// P for 32 keys held in registers (fp32 bits), written back in place over sv[0 .. 15] as bf16
+// pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds them to acc (the
+// fp32 values: only the product with V sees them in bf16).
+template <bool kAll>
+__device__ __forceinline__ void p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2, uint64_t (&acc)[2]) {
+#pragma unroll
+  for (int u = 0; u < 32; u += 2) {
+    float p0, p1;
+    f2_unpack(f2_fma(f2_pack(sv[u], sv[u + 1]), scale2, negm2), p0, p1);
+    p0 = ex2_approx(p0);
+    p1 = ex2_approx(p1);
+    if (!kAll) {
+      p0 = (u < lim) ? p0 : 0.f;
+      p1 = (u + 1 < lim) ? p1 : 0.f;
+    }
+    sv[u >> 1] = pack_bf16x2(p0, p1);
+    acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+  }
+}
+__device__ __forceinline__ void zero_quarter(uint32_t (&sv)[32]) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) sv[u] = 0u;
+}
+// Max of the first `lim` of 32 fp32 values.
+template <bool kAll>
+__device__ __forceinline__ float max_quarter(const uint32_t (&sv)[32], int lim) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int u = 0; u < 32; u += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int a = u + 2 * e;
+      mx[e] = max3f(mx[e], (kAll || a < lim) ? __uint_as_float(sv[a]) : -INFINITY,
+                    (kAll || a + 1 < lim) ? __uint_as_float(sv[a + 1]) : -INFINITY);
+    }
+  return max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+}
+
+// This thread's index, opaque to the compiler: what is derived from it is computed where it is
+// used instead of being kept in registers across the softmax loop. (Shared memory leaves almost
+// no L1, so a register that spills there costs a trip to L2 per chunk.)
+__device__ __forceinline__ int fresh_tid() {
+  int t;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+  return t;
+}
+
+// ---------------------------------------------------------------- builder
+template <class X, bool kSel>
+__device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea &A, const long long *pre, int lane) {
+  constexpr int H = X::kChunk / kHalf, kPer = 32 / H;  // bits per chunk, chunks per word
+  const int T = P.T, k = P.D.k, B = P.D.B, W = P.W;
+  const long long total = pre[P.nb];
+  const int C = ctas_of(P, total), c = blockIdx.x;
+  long long x = c < C ? range_start<X>(P, pre, total, C, c) : total;
+  const long long lo = x, hi = c < C ? range_start<X>(P, pre, total, C, c + 1) : total;
+  int sub = -1;  // with a selection: first chunk of the unit's next segment; the bits of one have room for kPer W
+  for (int su = 0;; ++su) {
+    const int s = su & 1;
+    if (su >= 2 && !idle_wait_warp(&A.free[s], ((su >> 1) - 1) & 1)) {
+      if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
+      *A.abort_flag = 1;
+      break;
+    }
+    UnitInfo &I = *(UnitInfo *)(A.info + s * kInfoBytes);
+    if (x >= hi || *A.abort_flag) {
+      if (lane == 0) I.live = 0;
+      __syncwarp();
+      mbar_arrive(&A.full[s]);
+      break;
+    }
+    const Unit r = unit_at<X>(P, pre, x);
+    const long long end = min(hi, r.first + r.w);
+    const int c_lo = (int)((x - r.first) / X::kChunk), c_hi = (int)((end - r.first + X::kChunk - 1) / X::kChunk);
+    const int ca = sub >= 0 ? sub : c_lo, cb = kSel ? min(c_hi, ca + kPer * W) : c_hi;
+    const int r0 = r.u * X::kTiles * T, n = r.q.s.n, t0 = r.q.s.len - n;
+    if (kSel) {
+      uint32_t *bits = (uint32_t *)(A.bits + s * kBitSlotBytes), *tile_bits = bits + kBitWords;
+      const int rows = min(X::kTiles * T, n - r0), h0 = H * ca, h1 = H * cb, per = B / kHalf;
+      // A token's bits, one token a lane: the halves of its selected blocks (an ascending list) and
+      // of its trailing range
+      for (int tok = lane; tok < X::kTiles * T; tok += 32) {
+        uint32_t *mine = bits + tok * W;
+        for (int i = 0; i < W; ++i) mine[i] = 0;
+        if (tok >= rows) continue;
+        const int t = t0 + r0 + tok, n_c = (t + 1) / B;
+        const int32_t *list = P.sel + ((size_t)r.q.s.q0 + r0 + tok) * k;
+        auto set = [&](int a, int z) {
+          for (int h = max(a, h0); h < min(z, h1); ++h) mine[(h - h0) >> 5] |= 1u << ((h - h0) & 31);
+        };
+#pragma unroll 4
+        for (int i = 0; i < k; ++i) {
+          const int j = list[i];
+          if (j >= 0 && j < n_c) set(j * per, j * per + per);
+        }
+        set(n_c * per, t / kHalf + 1);
+      }
+      __syncwarp();
+      for (int e = lane; e < X::kTiles * W; e += 32) {
+        const int w = e / W, i = e - w * W;
+        uint32_t any = 0;
+        for (int tok = 0; tok < T; ++tok) any |= bits[(w * T + tok) * W + i];
+        tile_bits[e] = any;
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      I.b = P.b0 + r.b;
+      I.g = r.g;
+      I.q0 = r.q.s.q0;
+      I.r0 = r0;
+      I.n = n;
+      I.len = r.q.s.len;
+      I.slot = c_lo == 0 && end == r.first + r.w ? -1 : 2 * c + (x == lo ? 0 : 1);
+      I.ca = ca;
+      I.cb = cb;
+      // every chunk up to the tile's last token
+      I.cend[0] = min(cb, (t0 + min(n, r0 + T) - 1) / X::kChunk + 1);
+      I.cend[1] = X::kTiles == 2 && r0 + T < n ? min(cb, (t0 + min(n, r0 + 2 * T) - 1) / X::kChunk + 1) : ca;
+      I.part = (ca == c_lo ? 1 : 0) | (cb == c_hi ? 2 : 0);
+      I.live = 1;
+    }
+    __syncwarp();
+    mbar_arrive(&A.full[s]);
+    if (cb == c_hi) x = end, sub = -1;
+    else sub = cb;
+  }
+}
+
+// ---------------------------------------------------------------- parts of a unit
+// Block (c, y): if the last unit of CTA c's range begins there and goes on in later ranges, its
+// rows 16 y .. 16 y + 15, one a warp at a time (128 elements of it a block: z): out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
+constexpr int kMergeWarps = 8, kMergeRows = 16;
+template <class X>
+__global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {
+  extern __shared__ long long s_pre[];
+  make_plan<X>(P, s_pre, nullptr);
+  pdl_wait();  // the parts come from the kernel before
+  const long long total = s_pre[P.nb];
+  const int C = ctas_of(P, total), c = blockIdx.x;
+  if (c + 1 >= C) return;
+  const long long cut = range_start<X>(P, s_pre, total, C, c + 1);
+  if (cut >= total) return;
+  const Unit r = unit_at<X>(P, s_pre, cut);
+  if (cut == r.first || cta_of(r.first, C, total) != c) return;
+  const int c_last = cta_of(r.first + (r.w - 1) / X::kChunk * X::kChunk, C, total);
+  const int s0 = 2 * c + (range_start<X>(P, s_pre, total, C, c) == r.first ? 0 : 1);
+  const int warp = threadIdx.x >> 5, col = blockIdx.z * 128 + (threadIdx.x & 31) * 4;
+  for (int e = warp; e < kMergeRows; e += kMergeWarps) {
+    const int rr = blockIdx.y * kMergeRows + e;  // tile rr / 128
+    const int row = rr % kRows;
+    const int tok = r.u * X::kTiles * P.T + rr / kRows * P.T + row / P.D.G;
+    if (row / P.D.G >= P.T || tok >= r.q.s.n) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = c; p <= c_last; ++p) {
+      const size_t at = (size_t)(p == c ? s0 : 2 * p) * (X::kTiles * kRows) + rr;
+      const float2 ml = *(const float2 *)(P.part_ml + at * 2);
+      if (ml.x == -INFINITY) continue;  // the part sees nothing of the row
+      const float4 x = *(const float4 *)(P.part_o + at * X::kD + col);
+      const float mn = fmaxf(m, ml.x);
+      const float fa = ex2_approx(m - mn), fb = ex2_approx(ml.x - mn);
+      o.x = fmaf(fb, x.x, o.x * fa);
+      o.y = fmaf(fb, x.y, o.y * fa);
+      o.z = fmaf(fb, x.z, o.z * fa);
+      o.w = fmaf(fb, x.w, o.w * fa);
+      l = fmaf(fb, ml.y, l * fa);
+      m = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    __nv_bfloat16 *dst = P.out + (((size_t)r.q.s.q0 + tok) * P.D.Hq + r.g * P.D.G + row % P.D.G) * X::kD + col;
+    *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)p;
+  }
+  return fn;
+}
+
+int sm_count() {
+  static int n[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n[dev] = 148;
+  return n[dev];
+}
+
+// 3-D bf16 tensor map of dense rows of d elements, 128-byte swizzle, zero fill out of bounds.
+bool make_map(CUtensorMap *m, const void *ptr, int d, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, d1, d2};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, d1 * d * 2};
+  cuuint32_t box[3] = {64, b1, b2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Fills P and calls launch(P, tk, tv, smem), then the merge, once per kMaxSeqs sequences; tk and
+// tv are the tensor maps of the pools.
+template <class X, typename Launch>
+cudaError_t launch_chunks(Launch launch, size_t (*smem_of)(bool, int), const Dims &D, const Paged &G, const void *q,
+                          const void *k_pages, const void *v_pages, const int32_t *sel, void *out, int min_rows,
+                          void *scratch, int *status, cudaStream_t st) {
+  if (!encode_fn()) {
+    note_error("cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
+    return cudaErrorNotSupported;
+  }
+  TcParams P;
+  P.D = D;
+  P.P = G;
+  P.sel = sel;
+  P.q = (const __nv_bfloat16 *)q;
+  P.out = (__nv_bfloat16 *)out;
+  P.part_o = (float *)scratch;
+  P.part_ml = P.part_o + (size_t)2 * kMaxCtas * X::kTiles * kRows * X::kD;
+  P.status = status;
+  P.T = kRows / D.G;
+  P.sl2 = D.scale * 1.4426950408889634f;
+  P.C = std::min(sm_count(), kMaxCtas);
+  P.min_rows = min_rows;
+  P.box = std::min(G.ps, X::kChunk);
+  P.W = std::min(kBitTileWords / X::kTiles, kBitWords / (X::kTiles * P.T));
+  P.W -= 1 - P.W % 2;  // odd: the builder's lanes, a token each, hit different banks
+  const uint64_t planes = (uint64_t)G.n_pages * D.Hkv;
+  CUtensorMap tk, tv;
+  if (!make_map(&tk, k_pages, X::kD, G.ps, planes, P.box, 1) || !make_map(&tv, v_pages, X::kD, G.ps, planes, P.box, 1)) {
+    note_error("paged attention tensor maps", cudaErrorInvalidValue);
+    return cudaErrorInvalidValue;
+  }
+  for (P.b0 = 0; P.b0 < G.batch; P.b0 += kMaxSeqs) {
+    P.nb = std::min(kMaxSeqs, G.batch - P.b0);
+    note_launch();
+    cudaError_t e = launch(P, tk, tv, smem_of(sel != nullptr, P.nb));
+    if (e == cudaSuccess) {
+      note_launch();
+      e = launch_maybe_pdl(k_paged_merge<X>, dim3(P.C, X::kTiles * kRows / kMergeRows, X::kD / 128),
+                           dim3(kMergeWarps * 32), (size_t)(P.nb + 1) * 8, st, true, P);
+    }
+    if (e != cudaSuccess) {
+      note_error("paged chunk attention launch", e);
+      return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+template <class X>
+size_t partials_bytes() {
+  return (size_t)2 * kMaxCtas * X::kTiles * kRows * (X::kD + 2) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace qsa

@@ -11,12 +11,8 @@
 // products read their operands at the full rate of shared memory, so tensor pipe, MUFU and
 // shared memory bound it together.
 //
-// Schedule: units differ in length and there may be fewer of them than SMs, so the keys that
-// the units see, laid end to end, are cut into C equal ranges, C = one per SM (fewer for
-// little work), and CTA c takes range c: no CTA waits for another, and at most the first and
-// the last unit of a range are shared with neighbours. A part of a unit leaves its
-// unnormalised O with (m, l) per row in the workspace, two slots per CTA, and k_paged_merge,
-// one row a warp, joins them in order. Inside a CTA the roles are pipelined across units:
+// The work is divided among the CTAs as qsa_paged_plan.cuh describes. Inside a CTA the roles are
+// pipelined across units:
 //   warp 0      TMA producer: Q, then K of chunk j and V of chunk j - 1 into ring entry j;
 //               its lanes hold the page numbers of the next chunk's boxes;
 //   warp 1      MMA issuer (TMEM owner): per chunk O_A += P_A V, S_A = Q_A K'^T, then B;
@@ -28,47 +24,32 @@
 //               the epilogue. Four warps a scheduler: with one thread a row the exponentials
 //               and the arithmetic around them did not overlap (1560-1610 us at 8K of 32K).
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
-#include <cuda.h>
-#include <math.h>
-
-#include <algorithm>
-
-#include "qsa_internal.h"
-#include "sm100_ptx.cuh"
+#include "qsa_paged_plan.cuh"
 
 namespace qsa {
 namespace {
 
-using namespace sm100;
-
 constexpr int kD = 128;      // head dim served
-constexpr int kRows = 128;   // MMA M: (token, head) rows per tile
 constexpr int kTiles = 2;    // tiles per unit
 constexpr int kChunk = 128;  // keys per chunk
-constexpr int kHalf = 64;    // mask granularity: the smallest block size served
 constexpr int kNE = 2;       // ring depth: entry j holds K of chunk j and V of chunk j - 1
+struct Two128 {
+  static constexpr int kD = qsa::kD, kTiles = qsa::kTiles, kChunk = qsa::kChunk;
+};
 constexpr int kThreads = 640;
 constexpr int kBuilderWarp = 2;
 constexpr int kSoftWarp0 = 4;  // first softmax warp
 constexpr int kSoftWarps = 16;
 constexpr uint32_t kTmemCols = 512;  // S of tile w at 128 w, O of tile w at 256 + 128 w
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMaxSeqs = 1024;   // sequences per launch
-constexpr int kMaxCtas = 152;
-constexpr int kMinKeys = 512;    // keys of a unit that make a CTA's range worth having
 
 constexpr uint32_t kQBytes = kRows * kD * 2;    // per tile, two 64-column halves
 constexpr uint32_t kKVBytes = kChunk * kD * 2;  // per K (or V) chunk, two halves
 constexpr uint32_t kEntryBytes = 2 * kKVBytes;
-constexpr int kBitWords = 2048;                 // words of a segment's token bits: 2 a chunk and token
-constexpr int kBitTileWords = 128;              // and of its tiles' bits
-constexpr uint32_t kBitSlotBytes = (kBitWords + kBitTileWords) * 4;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffE = kOffQ + kTiles * kQBytes;
 constexpr uint32_t kOffBar = kOffE + kNE * kEntryBytes;
 constexpr uint32_t kOffMisc = kOffBar + 256;
 constexpr uint32_t kOffInfo = kOffMisc + 64;
-constexpr uint32_t kInfoBytes = 64;
 constexpr uint32_t kOffBits = kOffInfo + 2 * kInfoBytes;  // with a selection: [slot] kBitSlotBytes
 
 // barrier slots
@@ -83,222 +64,6 @@ constexpr int kBarSlotFull = kBarPVDone + 2;    // [slot], the builder's 32 lane
 constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
 constexpr int kNumBars = kBarSlotFree + 2;
 static_assert(kNumBars * 8 <= 256, "barrier area");
-
-struct TcParams {
-  Dims D;
-  Paged P;
-  const int32_t *sel;  // null: every visible token
-  __nv_bfloat16 *out;
-  float *part_o;       // [2 C][kTiles * kRows][kD] unnormalised O
-  float *part_ml;      // [2 C][kTiles * kRows][2]
-  int *status;
-  int T;               // tokens per tile
-  float sl2;           // scale * log2(e)
-  int C;               // CTAs
-  int b0, nb;          // sequences of this launch
-  int min_rows;        // sequences with fewer (token, head) rows are left to the row kernel
-  int box;             // keys per TMA box: min(page size, kChunk)
-  int W;               // words of 16 chunks a token's bits have
-};
-
-// ---------------------------------------------------------------- the key list
-// The list of all units' visible keys: sequence by sequence, KV head by KV head, unit by unit.
-// Unit u of a sequence with n new tokens of len sees w(u) = len - n + min(n, (u + 1) 2T) keys.
-struct SeqPlan {
-  PagedSeq s;
-  int units;        // per KV head
-  long long keys;   // per KV head
-};
-__device__ __forceinline__ SeqPlan seq_plan(const TcParams &P, int b, int *status) {
-  SeqPlan q;
-  q.s = paged_seq(P.P, P.b0 + b, status);
-  if ((long long)q.s.n * P.D.G < P.min_rows) q.s.n = 0;
-  const int step = kTiles * P.T;
-  q.units = (q.s.n + step - 1) / step;
-  q.keys = 0;
-  if (q.units) {
-    const long long u = q.units - 1;
-    q.keys = u * (q.s.len - q.s.n) + (long long)P.T * u * (u + 1) + q.s.len;
-  }
-  return q;
-}
-// Keys of the units before u (u < units) of one KV head.
-__device__ __forceinline__ long long keys_before(const TcParams &P, const SeqPlan &q, long long u) {
-  return u * (q.s.len - q.s.n) + (long long)P.T * u * (u + 1);
-}
-
-// pre[b]: keys of the sequences before b, in shared memory. Every thread of the block calls it.
-__device__ void make_plan(const TcParams &P, long long *pre, int *status) {
-  __shared__ long long s_sum[32];
-  const int nt = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (P.nb + nt - 1) / nt;
-  const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
-  long long run = 0;
-  for (int b = a; b < z; ++b) {
-    run += seq_plan(P, b, status).keys * P.D.Hkv;
-    pre[b + 1] = run;
-  }
-  long long incl = run;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  if (threadIdx.x == 0) pre[0] = 0;
-  __syncthreads();
-  long long before = incl - run;
-  for (int w = 0; w < warp; ++w) before += s_sum[w];
-  for (int b = a; b < z; ++b) pre[b + 1] += before;
-  __syncthreads();
-}
-__device__ __forceinline__ int ctas_of(const TcParams &P, long long total) {
-  return (int)min((long long)P.C, (total + kMinKeys - 1) / kMinKeys);
-}
-
-struct Unit {
-  int b, g, u;
-  long long first;  // its first key's place in the list
-  int w;            // keys it sees
-  SeqPlan q;
-};
-__device__ __forceinline__ Unit unit_at(const TcParams &P, const long long *pre, long long x) {
-  Unit r;
-  int lo = 0, hi = P.nb;  // pre[lo] <= x < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  r.b = lo;
-  r.q = seq_plan(P, lo, nullptr);
-  const long long in = x - pre[lo];
-  r.g = (int)(in / r.q.keys);
-  const long long y = in - r.g * r.q.keys;
-  int ul = 0, uh = r.q.units;
-  while (uh - ul > 1) {
-    const int mid = (ul + uh) >> 1;
-    if (keys_before(P, r.q, mid) <= y) ul = mid;
-    else uh = mid;
-  }
-  r.u = ul;
-  r.first = pre[lo] + r.g * r.q.keys + keys_before(P, r.q, ul);
-  r.w = r.q.s.len - r.q.s.n + min(r.q.s.n, (ul + 1) * kTiles * P.T);
-  return r;
-}
-// Where CTA c's range begins: c / C of the list, moved up to the next chunk of its unit (or to
-// the unit's end).
-__device__ __forceinline__ long long range_start(const TcParams &P, const long long *pre, long long total, int C, int c) {
-  if (c >= C) return total;
-  const long long x = (long long)c * total / C;
-  const Unit r = unit_at(P, pre, x);
-  const long long y = (x - r.first + kChunk - 1) / kChunk * kChunk;
-  return r.first + min(y, (long long)r.w);
-}
-// The CTA whose range holds place x (a chunk's beginning): floor(c T / C) <= x < floor((c + 1) T / C).
-__device__ __forceinline__ int cta_of(long long x, int C, long long total) {
-  return (int)(((x + 1) * C + total - 1) / total) - 1;
-}
-
-// A segment as the builder hands it to the other warps.
-struct UnitInfo {
-  int live;  // 0: no segment left
-  int b, g, q0, r0, n, len;
-  int slot;  // partial slot, -1: the whole unit
-  int ca, cb;     // chunks [ca, cb)
-  int cend[2];    // without a selection tile w sees the chunks below cend[w]
-  int part;       // bit 0: the first of the unit's segments here, bit 1: the last
-};
-static_assert(sizeof(UnitInfo) <= kInfoBytes, "unit info area");
-
-// The chunks of a segment: of the unit (the union of its tiles') and of each tile. With a
-// selection bit 2 i + h of a bit list stands for half h of chunk ca + i.
-template <bool kSel>
-struct Chunks {
-  const uint32_t *bits;  // tile 0's words, then tile 1's
-  int nw, ca, cend[2];
-  __device__ __forceinline__ Chunks(const UnitInfo &I, const uint32_t *tile_bits, int W)
-      : bits(tile_bits), nw(W), ca(I.ca), cend{I.cend[0], I.cend[1]} {}
-  // Smallest chunk >= c of the unit, or -1.
-  __device__ __forceinline__ int next(int c) const {
-    if (!kSel) return c < max(cend[0], cend[1]) ? c : -1;
-    int w = (c - ca) >> 4;
-    if (w >= nw) return -1;
-    uint32_t x = (bits[w] | bits[nw + w]) & (0xffffffffu << (2 * ((c - ca) & 15)));
-    while (true) {
-      if (x) return ca + (w << 4) + ((__ffs(x) - 1) >> 1);
-      if (++w >= nw) return -1;
-      x = bits[w] | bits[nw + w];
-    }
-  }
-  __device__ __forceinline__ bool has(int w, int c) const {
-    return kSel ? (bits[w * nw + ((c - ca) >> 4)] >> (2 * ((c - ca) & 15))) & 3u : c < cend[w];
-  }
-};
-// A wait taken by a whole warp: the same answer on every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
-}
-// A wait off the critical path that sleeps between polls.
-__device__ __forceinline__ bool idle_wait_warp(uint64_t *bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  bool ok = true;
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitNs) {
-      ok = false;
-      break;
-    }
-    __nanosleep(128);
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-
-// P for 32 keys held in registers (fp32 bits), written back in place over sv[0 .. 15] as bf16
-// pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds them to acc (the
-// fp32 values: only the product with V sees them in bf16).
-template <bool kAll>
-__device__ __forceinline__ void p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2, uint64_t (&acc)[2]) {
-#pragma unroll
-  for (int u = 0; u < 32; u += 2) {
-    float p0, p1;
-    f2_unpack(f2_fma(f2_pack(sv[u], sv[u + 1]), scale2, negm2), p0, p1);
-    p0 = ex2_approx(p0);
-    p1 = ex2_approx(p1);
-    if (!kAll) {
-      p0 = (u < lim) ? p0 : 0.f;
-      p1 = (u + 1 < lim) ? p1 : 0.f;
-    }
-    sv[u >> 1] = pack_bf16x2(p0, p1);
-    acc[(u >> 1) & 1] = f2_add(acc[(u >> 1) & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-  }
-}
-__device__ __forceinline__ void zero_quarter(uint32_t (&sv)[32]) {
-#pragma unroll
-  for (int u = 0; u < 16; ++u) sv[u] = 0u;
-}
-// Max of the first `lim` of 32 fp32 values.
-template <bool kAll>
-__device__ __forceinline__ float max_quarter(const uint32_t (&sv)[32], int lim) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int u = 0; u < 32; u += 8)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int a = u + 2 * e;
-      mx[e] = max3f(mx[e], (kAll || a < lim) ? __uint_as_float(sv[a]) : -INFINITY,
-                    (kAll || a + 1 < lim) ? __uint_as_float(sv[a + 1]) : -INFINITY);
-    }
-  return max3f(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-}
-
-// This thread's index, opaque to the compiler: what is derived from it is computed where it is
-// used instead of being kept in registers across the softmax loop. (Shared memory leaves almost
-// no L1, so a register that spills there costs a trip to L2 per chunk.)
-__device__ __forceinline__ int fresh_tid() {
-  int t;
-  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
-  return t;
-}
 
 // A softmax thread's place: warp (tile w, lane group, sub-group) owns 16 rows of its tile; lane
 // t < 16 holds its row's first 64 keys of every chunk and the first 64 columns of its O, lane
@@ -318,89 +83,6 @@ __device__ __forceinline__ SoftPlace soft_place(int tid, int T, int G) {
   p.h = p.row % G;
   p.in_tile = p.row / G < T;
   return p;
-}
-
-// ---------------------------------------------------------------- builder
-template <bool kSel>
-__device__ __forceinline__ void build_segments(const TcParams &P, uint8_t *base, const long long *pre, int lane) {
-  uint64_t *bars = (uint64_t *)(base + kOffBar);
-  volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
-  const int T = P.T, k = P.D.k, B = P.D.B, W = P.W;
-  const long long total = pre[P.nb];
-  const int C = ctas_of(P, total), c = blockIdx.x;
-  long long x = c < C ? range_start(P, pre, total, C, c) : total;
-  const long long lo = x, hi = c < C ? range_start(P, pre, total, C, c + 1) : total;
-  int sub = -1;  // with a selection: first chunk of the unit's next segment; the bits of one have room for 16 W
-  for (int su = 0;; ++su) {
-    const int s = su & 1;
-    if (su >= 2 && !idle_wait_warp(&bars[kBarSlotFree + s], ((su >> 1) - 1) & 1)) {
-      if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
-      *abort_flag = 1;
-      break;
-    }
-    UnitInfo &I = *(UnitInfo *)(base + kOffInfo + s * kInfoBytes);
-    if (x >= hi || *abort_flag) {
-      if (lane == 0) I.live = 0;
-      __syncwarp();
-      mbar_arrive(&bars[kBarSlotFull + s]);
-      break;
-    }
-    const Unit r = unit_at(P, pre, x);
-    const long long end = min(hi, r.first + r.w);
-    const int c_lo = (int)((x - r.first) / kChunk), c_hi = (int)((end - r.first + kChunk - 1) / kChunk);
-    const int ca = sub >= 0 ? sub : c_lo, cb = kSel ? min(c_hi, ca + 16 * W) : c_hi;
-    const int r0 = r.u * kTiles * T, n = r.q.s.n, t0 = r.q.s.len - n;
-    if (kSel) {
-      uint32_t *bits = (uint32_t *)(base + kOffBits + s * kBitSlotBytes), *tile_bits = bits + kBitWords;
-      const int rows = min(kTiles * T, n - r0), h0 = 2 * ca, h1 = 2 * cb, per = B / kHalf;
-      // A token's bits, one token a lane: the halves of its selected blocks (an ascending list) and
-      // of its trailing range
-      for (int tok = lane; tok < kTiles * T; tok += 32) {
-        uint32_t *mine = bits + tok * W;
-        for (int i = 0; i < W; ++i) mine[i] = 0;
-        if (tok >= rows) continue;
-        const int t = t0 + r0 + tok, n_c = (t + 1) / B;
-        const int32_t *list = P.sel + ((size_t)r.q.s.q0 + r0 + tok) * k;
-        auto set = [&](int a, int z) {
-          for (int h = max(a, h0); h < min(z, h1); ++h) mine[(h - h0) >> 5] |= 1u << ((h - h0) & 31);
-        };
-#pragma unroll 4
-        for (int i = 0; i < k; ++i) {
-          const int j = list[i];
-          if (j >= 0 && j < n_c) set(j * per, j * per + per);
-        }
-        set(n_c * per, t / kHalf + 1);
-      }
-      __syncwarp();
-      for (int e = lane; e < kTiles * W; e += 32) {
-        const int w = e / W, i = e - w * W;
-        uint32_t any = 0;
-        for (int tok = 0; tok < T; ++tok) any |= bits[(w * T + tok) * W + i];
-        tile_bits[e] = any;
-      }
-      __syncwarp();
-    }
-    if (lane == 0) {
-      I.b = P.b0 + r.b;
-      I.g = r.g;
-      I.q0 = r.q.s.q0;
-      I.r0 = r0;
-      I.n = n;
-      I.len = r.q.s.len;
-      I.slot = c_lo == 0 && end == r.first + r.w ? -1 : 2 * c + (x == lo ? 0 : 1);
-      I.ca = ca;
-      I.cb = cb;
-      // every chunk up to the tile's last token
-      I.cend[0] = min(cb, (t0 + min(n, r0 + T) - 1) / kChunk + 1);
-      I.cend[1] = r0 + T < n ? min(cb, (t0 + min(n, r0 + 2 * T) - 1) / kChunk + 1) : ca;
-      I.part = (ca == c_lo ? 1 : 0) | (cb == c_hi ? 2 : 0);
-      I.live = 1;
-    }
-    __syncwarp();
-    mbar_arrive(&bars[kBarSlotFull + s]);
-    if (cb == c_hi) x = end, sub = -1;
-    else sub = cb;
-  }
 }
 
 template <bool kSel>
@@ -440,14 +122,15 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  make_plan(P, pre, blockIdx.x == 0 ? P.status : nullptr);
+  make_plan<Two128>(P, pre, blockIdx.x == 0 ? P.status : nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
   if (warp == kBuilderWarp) {
-    build_segments<kSel>(P, base, pre, lane);
+    const SlotArea area = {&bars[kBarSlotFull], &bars[kBarSlotFree], base + kOffInfo, base + kOffBits, abort_flag};
+    build_segments<Two128, kSel>(P, area, pre, lane);
   } else if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     // Lane i < 128 / box holds the pool plane (page, KV head) of the i-th box of the next chunk
@@ -465,7 +148,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const UnitInfo I = *info(s);
       if (!I.live) break;
       if (I.part & 1) have_q = false;
-      const Chunks<kSel> ch(I, token_bits(s) + kBitWords, P.W);
+      const Chunks<Two128, kSel> ch(I, token_bits(s) + kBitWords, P.W);
       const int t_hi = I.len - I.n + min(I.n, I.r0 + kTiles * T) - 1;  // the unit's last visible key
       auto plane = [&](int c) {
         int z = -1;
@@ -589,7 +272,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const int t_hi = info(s)->len - info(s)->n + min(info(s)->n, info(s)->r0 + kTiles * T) - 1;
       if (!live) break;
       if (part & 1) have_q = q_done = false, first0 = first1 = true;
-      const Chunks<kSel> ch(*info(s), token_bits(s) + kBitWords, P.W);
+      const Chunks<Two128, kSel> ch(*info(s), token_bits(s) + kBitWords, P.W);
       int c = ch.next(ch.ca);
       if (c >= 0) {
         if (!have_q) {
@@ -686,7 +369,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         m_ref = -INFINITY;
         l = 0.f;
       }
-      const Chunks<kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      const Chunks<Two128, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
       // A chunk whose last key is no further than t_free needs no mask per key: without a selection
       // the position of the warp's first row, with one the unit's last visible key.
       int t_free, t = 0, h_tail = 0;
@@ -863,88 +546,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   }
 }
 
-// ---------------------------------------------------------------- parts of a unit
-// Block (c, y): if the last unit of CTA c's range begins there and goes on in later ranges, its
-// rows 16 y .. 16 y + 15, one a warp at a time: out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
-constexpr int kMergeWarps = 8, kMergeRows = 16;
-__global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {
-  extern __shared__ long long s_pre[];
-  make_plan(P, s_pre, nullptr);
-  pdl_wait();  // the parts come from the kernel before
-  const long long total = s_pre[P.nb];
-  const int C = ctas_of(P, total), c = blockIdx.x;
-  if (c + 1 >= C) return;
-  const long long cut = range_start(P, s_pre, total, C, c + 1);
-  if (cut >= total) return;
-  const Unit r = unit_at(P, s_pre, cut);
-  if (cut == r.first || cta_of(r.first, C, total) != c) return;
-  const int c_last = cta_of(r.first + (r.w - 1) / kChunk * kChunk, C, total);
-  const int s0 = 2 * c + (range_start(P, s_pre, total, C, c) == r.first ? 0 : 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = warp; e < kMergeRows; e += kMergeWarps) {
-    const int rr = blockIdx.y * kMergeRows + e;  // tile rr / 128
-    const int row = rr % kRows;
-    const int tok = r.u * kTiles * P.T + rr / kRows * P.T + row / P.D.G;
-    if (row / P.D.G >= P.T || tok >= r.q.s.n) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = c; p <= c_last; ++p) {
-      const size_t at = (size_t)(p == c ? s0 : 2 * p) * (kTiles * kRows) + rr;
-      const float2 ml = *(const float2 *)(P.part_ml + at * 2);
-      if (ml.x == -INFINITY) continue;  // the part sees nothing of the row
-      const float4 x = *(const float4 *)(P.part_o + at * kD + lane * 4);
-      const float mn = fmaxf(m, ml.x);
-      const float fa = ex2_approx(m - mn), fb = ex2_approx(ml.x - mn);
-      o.x = fmaf(fb, x.x, o.x * fa);
-      o.y = fmaf(fb, x.y, o.y * fa);
-      o.z = fmaf(fb, x.z, o.z * fa);
-      o.w = fmaf(fb, x.w, o.w * fa);
-      l = fmaf(fb, ml.y, l * fa);
-      m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16 *dst = P.out + (((size_t)r.q.s.q0 + tok) * P.D.Hq + r.g * P.D.G + row % P.D.G) * kD + lane * 4;
-    *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  }
-}
-
 // ---------------------------------------------------------------- host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)p;
-  }
-  return fn;
-}
-
-int sm_count() {
-  static int n[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n[dev] = 148;
-  return n[dev];
-}
-
-// 3-D bf16 tensor map of dense rows of kD elements, 128-byte swizzle, zero fill out of bounds.
-bool make_map(CUtensorMap *m, const void *ptr, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
-  cuuint64_t dims[3] = {(cuuint64_t)kD, d1, d2};
-  cuuint64_t strides[2] = {(cuuint64_t)kD * 2, d1 * kD * 2};
-  cuuint32_t box[3] = {64, b1, b2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t smem_of(bool sel, int nb) {
   return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + (size_t)(nb + 1) * 8;
 }
@@ -952,61 +554,28 @@ static_assert(1024 + kOffBits + 2 * kBitSlotBytes + (kMaxSeqs + 1) * 8 <= 227 * 
 
 }  // namespace
 
-// bf16, head_dim 128, blocks of whole 64-key halves.
+// bf16, head_dim 128 or 256, blocks of whole 64-key halves.
 bool paged_tc_supported(const Dims &D, const Paged &G, bool sel) {
-  return D.bf16 && D.d == kD && D.G <= 32 && (!sel || D.B % kHalf == 0) &&
+  return D.bf16 && (D.d == 128 || D.d == 256) && D.G <= 32 && (!sel || D.B % kHalf == 0) &&
          (long long)G.n_pages * D.Hkv <= 0x7fffffffLL;
 }
 
-size_t paged_tc_workspace() { return (size_t)2 * kMaxCtas * kTiles * kRows * (kD + 2) * sizeof(float); }
+size_t paged_tc_workspace(const Dims &D) { return D.d == 256 ? paged_tc256_workspace() : partials_bytes<Two128>(); }
 
 cudaError_t launch_paged_tc(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
-  if (!encode_fn()) {
-    note_error("cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
-    return cudaErrorNotSupported;
-  }
-  TcParams P;
-  P.D = D;
-  P.P = G;
-  P.sel = sel;
-  P.out = (__nv_bfloat16 *)out;
-  P.part_o = (float *)scratch;
-  P.part_ml = P.part_o + (size_t)2 * kMaxCtas * kTiles * kRows * kD;
-  P.status = status;
-  P.T = kRows / D.G;
-  P.sl2 = D.scale * 1.4426950408889634f;
-  P.C = std::min(sm_count(), kMaxCtas);
-  P.min_rows = min_rows;
-  P.box = std::min(G.ps, kChunk);
-  P.W = std::min(kBitTileWords / kTiles, kBitWords / (kTiles * P.T));
-  CUtensorMap tq, tk, tv;
-  const uint64_t planes = (uint64_t)G.n_pages * D.Hkv;
-  if (!make_map(&tq, q, D.Hq, G.n_tok, D.G, P.T) || !make_map(&tk, k_pages, G.ps, planes, P.box, 1) ||
-      !make_map(&tv, v_pages, G.ps, planes, P.box, 1)) {
+  if (D.d == 256) return launch_paged_tc256(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+  CUtensorMap tq;
+  if (!encode_fn() || !make_map(&tq, q, kD, D.Hq, G.n_tok, D.G, kRows / D.G)) {
     note_error("paged attention tensor maps", cudaErrorInvalidValue);
     return cudaErrorInvalidValue;
   }
-  for (P.b0 = 0; P.b0 < G.batch; P.b0 += kMaxSeqs) {
-    P.nb = std::min(kMaxSeqs, G.batch - P.b0);
-    const size_t smem = smem_of(sel != nullptr, P.nb);
-    auto kern = sel ? k_paged_tc<true> : k_paged_tc<false>;
-    cudaError_t e = ensure_smem(kern, smem);
-    if (e == cudaSuccess) {
-      note_launch();
-      e = launch_maybe_pdl(kern, dim3(P.C), dim3(kThreads), smem, st, false, tq, tk, tv, P);
-    }
-    if (e == cudaSuccess) {
-      note_launch();
-      e = launch_maybe_pdl(k_paged_merge, dim3(P.C, kTiles * kRows / kMergeRows), dim3(kMergeWarps * 32),
-                           (size_t)(P.nb + 1) * 8, st, true, P);
-    }
-    if (e != cudaSuccess) {
-      note_error("paged chunk attention launch", e);
-      return e;
-    }
-  }
-  return cudaSuccess;
+  auto kern = sel ? k_paged_tc<true> : k_paged_tc<false>;
+  auto launch = [&](const TcParams &P, const CUtensorMap &tk, const CUtensorMap &tv, size_t smem) {
+    const cudaError_t e = ensure_smem(kern, smem);
+    return e == cudaSuccess ? launch_maybe_pdl(kern, dim3(P.C), dim3(kThreads), smem, st, false, tq, tk, tv, P) : e;
+  };
+  return launch_chunks<Two128>(launch, smem_of, D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
 }
 
 }  // namespace qsa

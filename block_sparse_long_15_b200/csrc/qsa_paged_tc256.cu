@@ -1,0 +1,470 @@
+// Attention of chunks of new tokens over a paged K/V cache on 5th-generation tensor cores
+// (tcgen05), head_dim 256: see qsa_paged_tc.cu for head_dim 128 and qsa_paged_plan.cuh for how
+// the work is divided.
+//
+// O of one 128-row tile takes 256 TMEM columns, so a CTA holds one tile: T = 128 / G tokens of
+// one KV head against 64-key chunks, 1024 clocks of products and 512 of exponentials each.
+// Q sits in TMEM too (128 columns): the QK product then reads only K from shared memory, at
+// half the rate that its 64 columns would need with both operands there, and shared memory is
+// left to six 32 KB stages of K and V. S is double-buffered, so the softmax of a chunk runs
+// beside the products of its neighbours:
+//   warp 0      TMA producer: K and V of a chunk into two 3-deep rings; 4 lanes per page box,
+//               one for each 64 columns;
+//   warp 1      MMA issuer (TMEM owner): O += P(n) V, S = Q K(n + 2)^T into the buffer that
+//               P(n) has just left;
+//   warp 2      builder;
+//   warps 4-11  softmax, 16 rows per warp, two threads a row with 32 logits each, Q of the next
+//               unit into TMEM, and the epilogue.
+// TMEM: O at 0, Q at 256, S (then P, in its first half) at 384 and 448.
+// Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
+#include "qsa_paged_plan.cuh"
+
+namespace qsa {
+namespace {
+
+struct One256 {
+  static constexpr int kD = 256, kTiles = 1, kChunk = 64;
+};
+constexpr int kD = One256::kD, kChunk = One256::kChunk;
+constexpr int kNR = 3;  // depth of each ring
+constexpr int kThreads = 384;
+constexpr int kBuilderWarp = 2;
+constexpr int kSoftWarp0 = 4;
+constexpr int kSoftWarps = 8;
+constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 384;
+
+constexpr uint32_t kStageBytes = kChunk * kD * 2;   // 4 groups of [64 rows][128 B]
+constexpr uint32_t kGroupBytes = kChunk * 128;
+constexpr uint32_t kOffK = 0;
+constexpr uint32_t kOffV = kOffK + kNR * kStageBytes;
+constexpr uint32_t kOffBar = kOffV + kNR * kStageBytes;
+constexpr uint32_t kOffMisc = kOffBar + 256;
+constexpr uint32_t kOffInfo = kOffMisc + 64;
+constexpr uint32_t kOffBits = kOffInfo + 2 * kInfoBytes;
+
+// barrier slots
+constexpr int kBarKFull = 0;
+constexpr int kBarKEmpty = kBarKFull + kNR;
+constexpr int kBarVFull = kBarKEmpty + kNR;
+constexpr int kBarVEmpty = kBarVFull + kNR;
+constexpr int kBarSFull = kBarVEmpty + kNR;     // [S buffer]
+constexpr int kBarPFull = kBarSFull + 2;        // [S buffer], 8 arrivals
+constexpr int kBarPVDone = kBarPFull + 2;       // a phase per PV
+constexpr int kBarODone = kBarPVDone + 1;       // a phase per unit: its last PV completed
+constexpr int kBarQFull = kBarODone + 1;        // a phase per unit: Q is in TMEM, 8 arrivals
+constexpr int kBarQEmpty = kBarQFull + 1;       // a phase per unit: its last QK completed
+constexpr int kBarSlotFull = kBarQEmpty + 1;    // [slot], the builder's 32 lanes
+constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
+constexpr int kNumBars = kBarSlotFree + 2;
+static_assert(kNumBars * 8 <= 256, "barrier area");
+
+template <bool kSel>
+__global__ void __launch_bounds__(kThreads, 1)
+k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ TcParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t *bars = (uint64_t *)(base + kOffBar);
+  uint32_t *tmem_slot = (uint32_t *)(base + kOffMisc);
+  volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
+  long long *pre = (long long *)(base + kOffBits + (kSel ? 2 * kBitSlotBytes : 0));
+
+  const Dims &D = P.D;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = P.T, G = D.G;
+  auto info = [&](int s) { return (const UnitInfo *)(base + kOffInfo + s * kInfoBytes); };
+  auto token_bits = [&](int s) { return (const uint32_t *)(base + kOffBits + s * kBitSlotBytes); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i == kBarPFull || i == kBarPFull + 1 || i == kBarQFull) count = kSoftWarps;
+      if (i == kBarSlotFull || i == kBarSlotFull + 1) count = 32;
+      if (i == kBarSlotFree || i == kBarSlotFree + 1) count = 2 + kSoftWarps;
+      mbar_init(&bars[i], count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  make_plan<One256>(P, pre, blockIdx.x == 0 ? P.status : nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp == kBuilderWarp) {
+    const SlotArea area = {&bars[kBarSlotFull], &bars[kBarSlotFree], base + kOffInfo, base + kOffBits, abort_flag};
+    build_segments<One256, kSel>(P, area, pre, lane);
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    // Lane 4 i + e < 4 * 64 / box holds the pool plane (page, KV head) of the i-th box of the next
+    // chunk (-1: no token there, or a page outside the pool) and loads its columns 64 e ..
+    const int n_lanes = 4 * (kChunk / P.box), box_i = lane >> 2, e = lane & 3;
+    const uint32_t box_bytes = (uint32_t)P.box * 128;
+    int j = 0;  // chunks so far
+    bool fail = false;
+    for (int su = 0; !fail; ++su) {
+      const int s = su & 1;
+      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+        fail = true;
+        break;
+      }
+      const UnitInfo I = *info(s);
+      if (!I.live) break;
+      const Chunks<One256, kSel> ch(I, token_bits(s) + kBitWords, P.W);
+      const int t_hi = I.len - I.n + min(I.n, I.r0 + T) - 1;  // the unit's last visible key
+      auto plane = [&](int c) {
+        int z = -1;
+        const int key = c * kChunk + box_i * P.box;
+        if (c >= 0 && lane < n_lanes && key <= t_hi) {
+          const int page = P.P.table[(size_t)I.b * P.P.max_pages + (key >> P.P.ps_shift)];
+          if (page >= 0 && page < P.P.n_pages) z = page * D.Hkv + I.g;
+          else record_status(P.status, QSA_ERR_DEVICE_CHECK);
+        }
+        return z;
+      };
+      int c = ch.next(ch.ca);
+      int z = plane(c);
+      while (c >= 0) {
+        const int cn = ch.next(c + 1), zn = plane(cn);  // read ahead
+        const int st = j % kNR, y = (c * kChunk + box_i * P.box) & (P.P.ps - 1);
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, z >= 0)) * box_bytes;
+        const uint32_t at = st * kStageBytes + e * kGroupBytes + box_i * box_bytes;
+        if (j >= kNR && !warp_wait(&bars[kBarKEmpty + st], ((j / kNR) & 1) ^ 1)) {
+          fail = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kBarKFull + st], bytes);
+        __syncwarp();
+        if (z >= 0) tma_load_3d(&tm_k, &bars[kBarKFull + st], base + kOffK + at, e * 64, y, z);
+        if (j >= kNR && !warp_wait(&bars[kBarVEmpty + st], ((j / kNR) & 1) ^ 1)) {
+          fail = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kBarVFull + st], bytes);
+        __syncwarp();
+        if (z >= 0) tma_load_3d(&tm_v, &bars[kBarVFull + st], base + kOffV + at, e * 64, y, z);
+        __syncwarp();
+        c = cn;
+        z = zn;
+        ++j;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+    }
+    if (fail) {
+      if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kChunk, false, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, kD, false, true);
+    const uint64_t k_desc0 = sdesc_sw128(smem_u32(base + kOffK), 16, 1024);
+    const uint64_t v_desc0 = sdesc_sw128(smem_u32(base + kOffV), kGroupBytes, 1024);
+    int nk = 0, nv = 0;  // QKs and PVs so far, over all units
+    int units = 0;
+    bool fail = false, first = true;  // the unit's next PV overwrites O
+    auto issue_qk = [&]() -> bool {   // S(nk) = Q K(nk)^T into S buffer nk % 2
+      const int st = nk % kNR;
+      if (!warp_wait(&bars[kBarKFull + st], (nk / kNR) & 1)) return false;
+      tc_fence_after();
+      const uint64_t kd = k_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+      const uint32_t d = tbase + kColS + (nk & 1) * kChunk;
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk)
+        mma_ts_w(d, tbase + kColQ + kk * 8, kd + (uint64_t)(((kk >> 2) * kGroupBytes + (kk & 3) * 32) >> 4), idesc_qk,
+                 kk > 0 ? 1u : 0u);
+      mma_commit_w(&bars[kBarSFull + (nk & 1)]);
+      mma_commit_w(&bars[kBarKEmpty + st]);
+      ++nk;
+      return true;
+    };
+    for (int su = 0; !fail; ++su) {
+      const int s = su & 1;
+      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+        fail = true;
+        break;
+      }
+      const UnitInfo *I = info(s);
+      const int live = I->live, part = I->part;
+      if (!live) break;
+      const Chunks<One256, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      const int t_hi = I->len - I->n + min(I->n, I->r0 + T) - 1;
+      if (part & 1) {
+        first = true;
+        if (!warp_wait(&bars[kBarQFull], units & 1)) {
+          fail = true;
+          break;
+        }
+        ++units;
+        tc_fence_after();
+      }
+      // c: the next PV's chunk, ca: the next QK's, which runs two ahead
+      int c = ch.next(ch.ca), ca = c;
+      bool q_done = false;
+      auto advance_qk = [&]() {
+        if (ca < 0 || !issue_qk()) return ca < 0;
+        ca = ch.next(ca + 1);
+        if (ca < 0 && (part & 2)) {
+          mma_commit_w(&bars[kBarQEmpty]);
+          q_done = true;
+        }
+        return true;
+      };
+      if (!advance_qk() || !advance_qk()) fail = true;
+      for (; c >= 0 && !fail; c = ch.next(c + 1)) {
+        const int st = nv % kNR;
+        if (!warp_wait(&bars[kBarVFull + st], (nv / kNR) & 1) ||
+            !warp_wait(&bars[kBarPFull + (nv & 1)], (nv >> 1) & 1)) {
+          fail = true;
+          break;
+        }
+        tc_fence_after();
+        // V rows behind the unit's last visible key are zeroed: their P is zero, but the slots (or
+        // what an unloaded box left) may hold NaN, and 0 * NaN is NaN.
+        const int valid_rows = t_hi + 1 - c * kChunk;
+        if (valid_rows < kChunk) {
+          uint8_t *vs = base + kOffV + st * kStageBytes;
+          for (int rr = max(valid_rows, 0) + lane; rr < kChunk; rr += 32)
+            for (int q = 0; q < 4; ++q) {
+              uint4 *p4 = (uint4 *)(vs + q * kGroupBytes + rr * 128);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) p4[x] = make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t vd = v_desc0 + (uint64_t)((st * kStageBytes) >> 4);
+        const uint32_t pcol = tbase + kColS + (nv & 1) * kChunk;
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          mma_ts_w(tbase, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        first = false;
+        mma_commit_w(&bars[kBarVEmpty + st]);
+        mma_commit_w(&bars[kBarPVDone]);
+        ++nv;
+        // S of two chunks on goes into the buffer that this PV reads; MMAs run in issue order
+        if (!advance_qk()) fail = true;
+      }
+      if (!fail && (part & 2)) {
+        if (!q_done) mma_commit_w(&bars[kBarQEmpty]);
+        mma_commit_w(&bars[kBarODone]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+    }
+    if (fail && lane == 0) {
+      record_status(P.status, QSA_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else if (warp >= kSoftWarp0) {
+    // ---------------------------------------------------------------- softmax + epilogue
+    // Warp (lane group, sub-group) owns 16 rows: thread t < 16 holds its row's first 32 keys of every
+    // chunk, dims 0 .. 127 of its Q and columns 0 .. 127 of its O, thread t + 16 the others.
+    const int row0 = 32 * (warp & 3) + 16 * ((warp - kSoftWarp0) >> 2);
+    const int hh = lane >> 4, row = row0 + (lane & 15);
+    const int tok = row / G, h = row % G;
+    const uint32_t lane_addr = tbase + ((uint32_t)row0 << 16);
+    const uint64_t scale2 = f2_splat(P.sl2);
+    int n_all = 0, units = 0;  // chunks and units so far
+    bool some = false;         // a chunk of this unit
+    float m_ref = -INFINITY, l = 0.f;
+    bool fail = false;
+    for (int su = 0; !fail; ++su) {
+      const int s = su & 1;
+      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+        fail = true;
+        break;
+      }
+      const UnitInfo *I = info(s);
+      if (!I->live) break;
+      const int part_of = I->part;
+      const int t0 = I->len - I->n + I->r0;  // the unit's first position
+      const bool valid = tok < T && I->r0 + tok < I->n;
+      const int t = valid ? t0 + tok : -1;
+      const size_t at = (((size_t)I->q0 + (valid ? I->r0 + tok : 0)) * D.Hq + I->g * G + h) * kD + hh * 128;
+      if (part_of & 1) {
+        some = false;
+        m_ref = -INFINITY;
+        l = 0.f;
+        // Q of the unit, once every QK of the unit before has completed
+        uint32_t q0[32], q1[32];
+        const uint4 *src = (const uint4 *)(P.q + at);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 a = valid ? src[i] : make_uint4(0, 0, 0, 0), b = valid ? src[i + 8] : make_uint4(0, 0, 0, 0);
+          q0[4 * i] = a.x, q0[4 * i + 1] = a.y, q0[4 * i + 2] = a.z, q0[4 * i + 3] = a.w;
+          q1[4 * i] = b.x, q1[4 * i + 1] = b.y, q1[4 * i + 2] = b.z, q1[4 * i + 3] = b.w;
+        }
+        if (units > 0 && !warp_wait(&bars[kBarQEmpty], (units - 1) & 1)) {
+          fail = true;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32_split<64>(lane_addr + kColQ, q0);
+        tmem_st32_split<64>(lane_addr + kColQ + 32, q1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarQFull]);
+        ++units;
+      }
+      const Chunks<One256, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      // A chunk whose last key is no further than t_free needs no mask per key: without a selection
+      // the position of the warp's first row, with one the unit's last visible key.
+      const int t_free = kSel ? t0 + min(I->n - I->r0, T) - 1 : t0 + row0 / G;
+      const int h_tail = kSel ? (t + 1) / D.B * (D.B / kHalf) : 0;  // the trailing range starts at this chunk
+      const uint32_t *my_bits = token_bits(s) + (valid ? tok : 0) * P.W;
+      for (int c = ch.next(ch.ca); c >= 0; c = ch.next(c + 1)) {
+        // this thread's first `lim` keys are visible: up to the position, or, in a selected block, all
+        int lim = min(max(t + 1 - c * kChunk - hh * 32, 0), 32);
+        bool part = c * kChunk + kChunk - 1 > t_free, any = true;
+        if (kSel) {
+          if (c < h_tail) lim = (my_bits[(c - ch.ca) >> 5] >> ((c - ch.ca) & 31)) & 1u ? 32 : 0;
+          part = part || __any_sync(0xffffffffu, lim > 0 && lim < 32);
+          any = __any_sync(0xffffffffu, lim > 0);
+        }
+        const uint32_t s_col = lane_addr + kColS + (n_all & 1) * kChunk;
+        if (!warp_wait(&bars[kBarSFull + (n_all & 1)], (n_all >> 1) & 1)) {
+          fail = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[32];
+        float mx = -INFINITY;
+        if (any) {
+          tmem_ld32_split<32>(s_col, sv);
+          tmem_ld_wait();
+          mx = part ? max_quarter<false>(sv, lim) : max_quarter<true>(sv, 32);
+          if (kSel && lim == 0) mx = -INFINITY;
+        }
+        const float cmax = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * P.sl2;
+        bool rescale = false;
+        float alpha = 1.f;
+        if (cmax > -INFINITY) {
+          if (m_ref == -INFINITY) {
+            m_ref = cmax;
+          } else if (cmax > m_ref + 8.f) {
+            rescale = true;
+            alpha = ex2_approx(m_ref - cmax);
+            m_ref = cmax;
+          }
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // A row that had a reference had a chunk before. S of this chunk being there proves the PV
+          // before the last complete, so one parity wait covers the last; the next one waits for
+          // this warp's arrival below.
+          if (!warp_wait(&bars[kBarPVDone], (n_all - 1) & 1)) {
+            fail = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int cb = 0; cb < 4; ++cb) {
+            uint32_t ov[32];
+            tmem_ld32_split<128>(lane_addr + cb * 32, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
+            tmem_st32_split<128>(lane_addr + cb * 32, ov);
+          }
+          l *= alpha;
+        }
+        uint64_t acc[2] = {0, 0};
+        if (any) {
+          // a thread that sees none of its keys takes +inf as its reference: p = 0
+          const uint64_t negm2 = f2_splat(!kSel || part || lim ? -m_ref : -INFINITY);
+          if (part) p_quarter<false>(sv, lim, scale2, negm2, acc);
+          else p_quarter<true>(sv, 32, scale2, negm2, acc);
+        } else {
+          zero_quarter(sv);
+        }
+        tmem_st16_split_lo<16>(s_col, sv);
+        float sum0, sum1;
+        f2_unpack(f2_add(acc[0], acc[1]), sum0, sum1);
+        l += sum0 + sum1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarPFull + (n_all & 1)]);
+        some = true;
+        ++n_all;
+      }
+      if ((part_of & 2) || fail) {
+        const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both key ranges
+        // ------------------------------------------------------------ epilogue
+        const bool have_o = !fail && warp_wait(&bars[kBarODone], (units - 1) & 1) && some;
+        if (!have_o && some && !fail) fail = true;
+        if (fail) {
+          if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        tc_fence_after();
+        const bool keep = have_o && lt > 0.f;  // a row that sees nothing is written as zeros
+        const int slot = I->slot;
+        const float inv = keep ? 1.f / lt : 0.f;
+        const size_t pr = (size_t)max(slot, 0) * kRows + row;
+        if (slot >= 0 && valid && hh == 0)
+          *(float2 *)(P.part_ml + pr * 2) = make_float2(keep ? m_ref : -INFINITY, keep ? lt : 0.f);
+#pragma unroll 1
+        for (int cb = 0; cb < 8; ++cb) {
+          uint32_t ov[16];
+          __syncwarp();
+          if (have_o) {  // the same for the whole warp
+            tmem_ld16_split<128>(lane_addr + cb * 16, ov);
+            tmem_ld_wait();
+          }
+          if (valid && slot < 0) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              pk[q] = keep ? pack_bf16x2(__uint_as_float(ov[2 * q]) * inv, __uint_as_float(ov[2 * q + 1]) * inv) : 0u;
+            uint4 *o4 = (uint4 *)(P.out + at + cb * 16);
+            o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          } else if (valid && have_o) {
+            uint4 *o4 = (uint4 *)(P.part_o + pr * kD + hh * 128 + cb * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o4[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+size_t smem_of(bool sel, int nb) { return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + (size_t)(nb + 1) * 8; }
+static_assert(1024 + kOffBits + 2 * kBitSlotBytes + (kMaxSeqs + 1) * 8 <= 227 * 1024, "shared memory");
+
+}  // namespace
+
+size_t paged_tc256_workspace() { return partials_bytes<One256>(); }
+
+cudaError_t launch_paged_tc256(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
+  auto kern = sel ? k_paged_tc256<true> : k_paged_tc256<false>;
+  auto launch = [&](const TcParams &P, const CUtensorMap &tk, const CUtensorMap &tv, size_t smem) {
+    const cudaError_t e = ensure_smem(kern, smem);
+    return e == cudaSuccess ? launch_maybe_pdl(kern, dim3(P.C), dim3(kThreads), smem, st, false, tk, tv, P) : e;
+  };
+  return launch_chunks<One256>(launch, smem_of, D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+}
+
+}  // namespace qsa
