@@ -534,10 +534,15 @@ qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRop
   return QSA_OK;
 }
 
-constexpr int kChunkRows = 64;
-bool paged_chunks(const Dims &D, const Paged &G) { return D.bf16 && (long long)G.max_chunk * D.G >= kChunkRows; }
+// A sequence with this many (token, head) rows goes to the tensor-core kernel.
+int chunk_rows(const Dims &D, bool sel) { return sel ? 64 : D.d == 256 ? 9 : 17; }
+bool use_paged_tc(const Dims &D, const Paged &G, bool sel) {
+  return (long long)G.max_chunk * D.G >= chunk_rows(D, sel) && paged_tc_supported(D, G, sel);
+}
+// The workspace serves both forms of the call.
 size_t paged_scratch(const Dims &D, const Paged &G) {
-  return round256(paged_rows_workspace(D)) + (paged_chunks(D, G) ? round256(paged_tc_workspace(D)) : 0);
+  const bool tc = use_paged_tc(D, G, false) || use_paged_tc(D, G, true);
+  return round256(paged_rows_workspace(D)) + (tc ? round256(paged_tc_workspace(D)) : 0);
 }
 
 // A packed tensor of rows of `width` elements, `row` elements apart.
@@ -645,14 +650,15 @@ qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, cons
   char *scratch = (char *)workspace + kStatusBytes;
   int *status = status_word(workspace);
   cudaStream_t st = (cudaStream_t)stream;
-  // Sequences with kChunkRows or more (token, head) rows go to the tensor-core kernel where it
-  // serves the shape, the others to the row kernel.
+  // Sequences with many (token, head) rows go to the tensor-core kernel where it serves the shape,
+  // the others to the row kernel; a single sequence to one of them.
   long long rows_below = 1LL << 62;
-  if (paged_chunks(D, G) && paged_tc_supported(D, G, sel != nullptr)) {
-    s = cuda_status(launch_paged_tc(D, G, q, k_pages, v_pages, sel, out, kChunkRows,
+  if (use_paged_tc(D, G, sel != nullptr)) {
+    const int from = G.batch == 1 ? 1 : chunk_rows(D, sel != nullptr);
+    s = cuda_status(launch_paged_tc(D, G, q, k_pages, v_pages, sel, out, from,
                                     scratch + round256(paged_rows_workspace(D)), status, st));
-    if (s != QSA_OK) return s;
-    rows_below = kChunkRows;
+    if (s != QSA_OK || from == 1) return s;
+    rows_below = from;
   }
   return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, rows_below, scratch, status, st));
 }

@@ -25,13 +25,20 @@ using namespace sm100;
 constexpr int kRows = 128;  // MMA M: (token, head) rows per tile
 constexpr int kHalf = 64;   // mask granularity: the smallest block size served
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMaxSeqs = 1024;  // sequences per launch
+constexpr int kMaxSeqs = 512;   // sequences per launch: their geometry sits in shared memory
 constexpr int kMaxCtas = 152;
 constexpr int kMinKeys = 512;   // keys of a unit that make a CTA's range worth having
 constexpr int kBitWords = 2048;     // words of a segment's token bits
 constexpr int kBitTileWords = 128;  // and of its tiles' bits
 constexpr uint32_t kBitSlotBytes = (kBitWords + kBitTileWords) * 4;
 constexpr uint32_t kInfoBytes = 64;
+
+// A unit to be joined from the parts that CTAs c .. c_last left: the first in slot s0, the others
+// in slots 2 p.
+struct MergeJob {
+  int c_last, s0;  // c_last < 0: none
+  int q0, r0, n, g;
+};
 
 struct TcParams {
   Dims D;
@@ -41,6 +48,7 @@ struct TcParams {
   __nv_bfloat16 *out;
   float *part_o;       // [2 C][rows of a unit][d] unnormalised O
   float *part_ml;      // [2 C][rows of a unit][2]: m (log2 domain), l
+  MergeJob *jobs;  // [C] of the unit that begins in CTA c and goes on in others
   int *status;
   int T;               // tokens per tile
   float sl2;           // scale * log2(e)
@@ -53,43 +61,49 @@ struct TcParams {
 
 // ---------------------------------------------------------------- the key list
 // The list of all units' visible keys: sequence by sequence, KV head by KV head, unit by unit.
-// Unit u of a sequence with n new tokens of len sees w(u) = len - n + min(n, (u + 1) step) keys, step = tiles * T tokens.
-struct SeqPlan {
-  PagedSeq s;
-  int units;        // per KV head
-  long long keys;   // per KV head
+// Unit u of a sequence with n new tokens of len sees w(u) = len - n + min(n, (u + 1) step) keys,
+// step = tiles * T tokens. In shared memory: keys before each sequence, and the geometry.
+struct SeqGeo {
+  int q0, n, len;  // n = 0: nothing to do here
 };
-template <class X>
-__device__ __forceinline__ SeqPlan seq_plan(const TcParams &P, int b, int *status) {
-  SeqPlan q;
-  q.s = paged_seq(P.P, P.b0 + b, status);
-  if ((long long)q.s.n * P.D.G < P.min_rows) q.s.n = 0;
-  const int step = X::kTiles * P.T;
-  q.units = (q.s.n + step - 1) / step;
-  q.keys = 0;
-  if (q.units) {
-    const long long u = q.units - 1;
-    q.keys = u * (q.s.len - q.s.n) + (long long)step * u * (u + 1) / 2 + q.s.len;
-  }
-  return q;
-}
-// Keys of the units before u (u < units) of one KV head.
-template <class X>
-__device__ __forceinline__ long long keys_before(const TcParams &P, const SeqPlan &q, long long u) {
-  return u * (q.s.len - q.s.n) + (long long)X::kTiles * P.T * u * (u + 1) / 2;
+struct PlanArea {
+  long long *pre;  // [nb + 1]
+  SeqGeo *seq;     // [nb]
+};
+__host__ __device__ constexpr size_t plan_bytes(int nb) { return (size_t)(nb + 1) * 8 + (size_t)nb * sizeof(SeqGeo); }
+
+// Divisions here have 64-bit operands that nearly always fit 32 bits, where they are much cheaper.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// pre[b]: keys of the sequences before b, in shared memory. Every thread of the block calls it.
+// Keys of the units before u of one KV head (u = units: all of them).
 template <class X>
-__device__ void make_plan(const TcParams &P, long long *pre, int *status) {
+__device__ __forceinline__ long long keys_before(const TcParams &P, const SeqGeo &q, int u) {
+  const int step = X::kTiles * P.T;
+  const long long k = (long long)u * (q.len - q.n) + (long long)step * u * (u + 1) / 2;
+  return (long long)u * step > q.n ? k - ((long long)u * step - q.n) : k;  // the last unit may be short
+}
+template <class X>
+__device__ __forceinline__ int units_of(const TcParams &P, const SeqGeo &q) {
+  const int step = X::kTiles * P.T;
+  return (q.n + step - 1) / step;
+}
+
+// Fills the plan. Every thread of the block calls it.
+template <class X>
+__device__ void make_plan(const TcParams &P, const PlanArea &L, int *status) {
   __shared__ long long s_sum[32];
   const int nt = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (P.nb + nt - 1) / nt;
   const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
   long long run = 0;
   for (int b = a; b < z; ++b) {
-    run += seq_plan<X>(P, b, status).keys * P.D.Hkv;
-    pre[b + 1] = run;
+    const PagedSeq q = paged_seq(P.P, P.b0 + b, status);
+    SeqGeo g = {q.q0, (long long)q.n * P.D.G < P.min_rows ? 0 : q.n, q.len};
+    L.seq[b] = g;
+    run += keys_before<X>(P, g, units_of<X>(P, g)) * P.D.Hkv;
+    L.pre[b + 1] = run;
   }
   long long incl = run;
 #pragma unroll
@@ -98,11 +112,11 @@ __device__ void make_plan(const TcParams &P, long long *pre, int *status) {
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_sum[warp] = incl;
-  if (threadIdx.x == 0) pre[0] = 0;
+  if (threadIdx.x == 0) L.pre[0] = 0;
   __syncthreads();
   long long before = incl - run;
   for (int w = 0; w < warp; ++w) before += s_sum[w];
-  for (int b = a; b < z; ++b) pre[b + 1] += before;
+  for (int b = a; b < z; ++b) L.pre[b + 1] += before;
   __syncthreads();
 }
 __device__ __forceinline__ int ctas_of(const TcParams &P, long long total) {
@@ -113,46 +127,46 @@ struct Unit {
   int b, g, u;
   long long first;  // its first key's place in the list
   int w;            // keys it sees
-  SeqPlan q;
+  SeqGeo s;
 };
 template <class X>
-__device__ __forceinline__ Unit unit_at(const TcParams &P, const long long *pre, long long x) {
+__device__ __forceinline__ Unit unit_at(const TcParams &P, const PlanArea &L, long long x) {
   Unit r;
   int lo = 0, hi = P.nb;  // pre[lo] <= x < pre[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= x) lo = mid;
+    if (L.pre[mid] <= x) lo = mid;
     else hi = mid;
   }
   r.b = lo;
-  r.q = seq_plan<X>(P, lo, nullptr);
-  const long long in = x - pre[lo];
-  r.g = (int)(in / r.q.keys);
-  const long long y = in - r.g * r.q.keys;
-  int ul = 0, uh = r.q.units;
+  r.s = L.seq[lo];
+  const long long per_head = div_pos(L.pre[lo + 1] - L.pre[lo], P.D.Hkv), in = x - L.pre[lo];
+  r.g = (int)div_pos(in, per_head);
+  const long long y = in - r.g * per_head;
+  int ul = 0, uh = units_of<X>(P, r.s);
   while (uh - ul > 1) {
     const int mid = (ul + uh) >> 1;
-    if (keys_before<X>(P, r.q, mid) <= y) ul = mid;
+    if (keys_before<X>(P, r.s, mid) <= y) ul = mid;
     else uh = mid;
   }
   r.u = ul;
-  r.first = pre[lo] + r.g * r.q.keys + keys_before<X>(P, r.q, ul);
-  r.w = r.q.s.len - r.q.s.n + min(r.q.s.n, (ul + 1) * X::kTiles * P.T);
+  r.first = L.pre[lo] + r.g * per_head + keys_before<X>(P, r.s, ul);
+  r.w = r.s.len - r.s.n + min(r.s.n, (ul + 1) * X::kTiles * P.T);
   return r;
 }
 // Where CTA c's range begins: c / C of the list, moved up to the next chunk of its unit (or to
 // the unit's end).
 template <class X>
-__device__ __forceinline__ long long range_start(const TcParams &P, const long long *pre, long long total, int C, int c) {
+__device__ __forceinline__ long long range_start(const TcParams &P, const PlanArea &L, long long total, int C, int c) {
   if (c >= C) return total;
-  const long long x = (long long)c * total / C;
-  const Unit r = unit_at<X>(P, pre, x);
-  const long long y = (x - r.first + X::kChunk - 1) / X::kChunk * X::kChunk;
-  return r.first + min(y, (long long)r.w);
+  const long long x = div_pos((long long)c * total, C);
+  const Unit r = unit_at<X>(P, L, x);
+  const int y = ((int)(x - r.first) + X::kChunk - 1) / X::kChunk * X::kChunk;
+  return r.first + min(y, r.w);
 }
 // The CTA whose range holds place x (a chunk's beginning): floor(c T / C) <= x < floor((c + 1) T / C).
 __device__ __forceinline__ int cta_of(long long x, int C, long long total) {
-  return (int)(((x + 1) * C + total - 1) / total) - 1;
+  return (int)div_pos((x + 1) * C + total - 1, total) - 1;
 }
 
 // A segment as the builder hands it to the other warps.
@@ -268,13 +282,16 @@ __device__ __forceinline__ int fresh_tid() {
 
 // ---------------------------------------------------------------- builder
 template <class X, bool kSel>
-__device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea &A, const long long *pre, int lane) {
+__device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea &A, const PlanArea &L, int lane) {
   constexpr int H = X::kChunk / kHalf, kPer = 32 / H;  // bits per chunk, chunks per word
   const int T = P.T, k = P.D.k, B = P.D.B, W = P.W;
-  const long long total = pre[P.nb];
+  const long long total = L.pre[P.nb];
   const int C = ctas_of(P, total), c = blockIdx.x;
-  long long x = c < C ? range_start<X>(P, pre, total, C, c) : total;
-  const long long lo = x, hi = c < C ? range_start<X>(P, pre, total, C, c + 1) : total;
+  // lane 0 and lane 1 look for the two ends of the range
+  const long long ends = c < C ? range_start<X>(P, L, total, C, c + (lane & 1)) : total;
+  long long x = __shfl_sync(0xffffffffu, ends, 0);
+  const long long lo = x, hi = __shfl_sync(0xffffffffu, ends, 1);
+  MergeJob job = {-1, 0, 0, 0, 0, 0};
   int sub = -1;  // with a selection: first chunk of the unit's next segment; the bits of one have room for kPer W
   for (int su = 0;; ++su) {
     const int s = su & 1;
@@ -290,48 +307,54 @@ __device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea
       mbar_arrive(&A.full[s]);
       break;
     }
-    const Unit r = unit_at<X>(P, pre, x);
+    const Unit r = unit_at<X>(P, L, x);
     const long long end = min(hi, r.first + r.w);
     const int c_lo = (int)((x - r.first) / X::kChunk), c_hi = (int)((end - r.first + X::kChunk - 1) / X::kChunk);
     const int ca = sub >= 0 ? sub : c_lo, cb = kSel ? min(c_hi, ca + kPer * W) : c_hi;
-    const int r0 = r.u * X::kTiles * T, n = r.q.s.n, t0 = r.q.s.len - n;
+    const int r0 = r.u * X::kTiles * T, n = r.s.n, t0 = r.s.len - n;
     if (kSel) {
       uint32_t *bits = (uint32_t *)(A.bits + s * kBitSlotBytes), *tile_bits = bits + kBitWords;
       const int rows = min(X::kTiles * T, n - r0), h0 = H * ca, h1 = H * cb, per = B / kHalf;
-      // A token's bits, one token a lane: the halves of its selected blocks (an ascending list) and
-      // of its trailing range
-      for (int tok = lane; tok < X::kTiles * T; tok += 32) {
-        uint32_t *mine = bits + tok * W;
-        for (int i = 0; i < W; ++i) mine[i] = 0;
-        if (tok >= rows) continue;
-        const int t = t0 + r0 + tok, n_c = (t + 1) / B;
-        const int32_t *list = P.sel + ((size_t)r.q.s.q0 + r0 + tok) * k;
-        auto set = [&](int a, int z) {
-          for (int h = max(a, h0); h < min(z, h1); ++h) mine[(h - h0) >> 5] |= 1u << ((h - h0) & 31);
-        };
-#pragma unroll 4
-        for (int i = 0; i < k; ++i) {
-          const int j = list[i];
-          if (j >= 0 && j < n_c) set(j * per, j * per + per);
-        }
-        set(n_c * per, t / kHalf + 1);
-      }
+      for (int i = lane; i < kBitWords + X::kTiles * W; i += 32) bits[i] = 0;
       __syncwarp();
-      for (int e = lane; e < X::kTiles * W; e += 32) {
-        const int w = e / W, i = e - w * W;
-        uint32_t any = 0;
-        for (int tok = 0; tok < T; ++tok) any |= bits[(w * T + tok) * W + i];
-        tile_bits[e] = any;
+      // Bits [a, z) of a token and of its tile, 4 at most (a block is 256 keys at most)
+      auto set = [&](int tok, int a, int z) {
+        a = max(a, h0), z = min(z, h1);
+        if (a >= z) return;
+        const uint64_t m = (uint64_t)((1u << (z - a)) - 1u) << ((a - h0) & 31);
+        const int w = (a - h0) >> 5, tile = tok < T ? 0 : W;
+        atomicOr(&bits[tok * W + w], (uint32_t)m);
+        atomicOr(&tile_bits[tile + w], (uint32_t)m);
+        if (m >> 32) {
+          atomicOr(&bits[tok * W + w + 1], (uint32_t)(m >> 32));
+          atomicOr(&tile_bits[tile + w + 1], (uint32_t)(m >> 32));
+        }
+      };
+      // the lists, 32 entries of kLists tokens at a time, and the trailing ranges
+      constexpr int kLists = 8;
+      const int32_t *lists = P.sel + ((size_t)r.s.q0 + r0) * k;
+      for (int tok = 0; tok < rows; tok += kLists)
+        for (int i = lane; i < k; i += 32) {
+          int j[kLists];
+#pragma unroll
+          for (int e = 0; e < kLists; ++e) j[e] = tok + e < rows ? lists[(tok + e) * k + i] : -1;
+#pragma unroll
+          for (int e = 0; e < kLists; ++e)
+            if (j[e] >= 0 && j[e] < (t0 + r0 + tok + e + 1) / B) set(tok + e, j[e] * per, j[e] * per + per);
+        }
+      for (int tok = lane; tok < rows; tok += 32) {
+        const int t = t0 + r0 + tok;
+        set(tok, (t + 1) / B * per, t / kHalf + 1);
       }
       __syncwarp();
     }
     if (lane == 0) {
       I.b = P.b0 + r.b;
       I.g = r.g;
-      I.q0 = r.q.s.q0;
+      I.q0 = r.s.q0;
       I.r0 = r0;
       I.n = n;
-      I.len = r.q.s.len;
+      I.len = r.s.len;
       I.slot = c_lo == 0 && end == r.first + r.w ? -1 : 2 * c + (x == lo ? 0 : 1);
       I.ca = ca;
       I.cb = cb;
@@ -343,56 +366,70 @@ __device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea
     }
     __syncwarp();
     mbar_arrive(&A.full[s]);
+    if (c_lo == 0 && end < r.first + r.w)
+      job = {cta_of(r.first + (r.w - 1) / X::kChunk * X::kChunk, C, total), 2 * c + (x == lo ? 0 : 1), r.s.q0, r0, n, r.g};
     if (cb == c_hi) x = end, sub = -1;
     else sub = cb;
   }
+  if (lane == 0) P.jobs[c] = job;
 }
 
 // ---------------------------------------------------------------- parts of a unit
-// Block (c, y): if the last unit of CTA c's range begins there and goes on in later ranges, its
-// rows 16 y .. 16 y + 15, one a warp at a time (128 elements of it a block: z): out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
-constexpr int kMergeWarps = 8, kMergeRows = 16;
+// Block (c, y, z): rows kMergeRows y .. of the unit that begins in CTA c's range and goes on in
+// later ones, 128 elements of each from 128 z on, a row a warp. Lane p holds the statistics of part
+// p, so that all parts' rows can be read at once:
+//   out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
+constexpr int kMergeWarps = 16, kMergeRows = kMergeWarps;
 template <class X>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {
-  extern __shared__ long long s_pre[];
-  make_plan<X>(P, s_pre, nullptr);
   pdl_wait();  // the parts come from the kernel before
-  const long long total = s_pre[P.nb];
-  const int C = ctas_of(P, total), c = blockIdx.x;
-  if (c + 1 >= C) return;
-  const long long cut = range_start<X>(P, s_pre, total, C, c + 1);
-  if (cut >= total) return;
-  const Unit r = unit_at<X>(P, s_pre, cut);
-  if (cut == r.first || cta_of(r.first, C, total) != c) return;
-  const int c_last = cta_of(r.first + (r.w - 1) / X::kChunk * X::kChunk, C, total);
-  const int s0 = 2 * c + (range_start<X>(P, s_pre, total, C, c) == r.first ? 0 : 1);
-  const int warp = threadIdx.x >> 5, col = blockIdx.z * 128 + (threadIdx.x & 31) * 4;
-  for (int e = warp; e < kMergeRows; e += kMergeWarps) {
-    const int rr = blockIdx.y * kMergeRows + e;  // tile rr / 128
-    const int row = rr % kRows;
-    const int tok = r.u * X::kTiles * P.T + rr / kRows * P.T + row / P.D.G;
-    if (row / P.D.G >= P.T || tok >= r.q.s.n) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = c; p <= c_last; ++p) {
-      const size_t at = (size_t)(p == c ? s0 : 2 * p) * (X::kTiles * kRows) + rr;
-      const float2 ml = *(const float2 *)(P.part_ml + at * 2);
-      if (ml.x == -INFINITY) continue;  // the part sees nothing of the row
-      const float4 x = *(const float4 *)(P.part_o + at * X::kD + col);
-      const float mn = fmaxf(m, ml.x);
-      const float fa = ex2_approx(m - mn), fb = ex2_approx(ml.x - mn);
-      o.x = fmaf(fb, x.x, o.x * fa);
-      o.y = fmaf(fb, x.y, o.y * fa);
-      o.z = fmaf(fb, x.z, o.z * fa);
-      o.w = fmaf(fb, x.w, o.w * fa);
-      l = fmaf(fb, ml.y, l * fa);
-      m = mn;
+  const int c = blockIdx.x;
+  const MergeJob J = P.jobs[c];
+  if (J.c_last < 0) return;
+  const int lane = threadIdx.x & 31, col = blockIdx.z * 128 + lane * 4;
+  const int rr = blockIdx.y * kMergeRows + (threadIdx.x >> 5), row = rr % kRows;  // row of tile rr / 128
+  const int tok = J.r0 + rr / kRows * P.T + row / P.D.G;
+  if (row / P.D.G >= P.T || tok >= J.n) return;
+  auto place = [&](int p) { return (size_t)(p == c ? J.s0 : 2 * p) * (X::kTiles * kRows) + rr; };
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = c; p0 <= J.c_last; p0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (p0 + lane <= J.c_last) ml = *(const float2 *)(P.part_ml + place(p0 + lane) * 2);
+    float mn = fmaxf(m, ml.x);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, s));
+    if (mn == -INFINITY) continue;  // none of these parts sees a key of the row
+    const float fa = ex2_approx(m - mn), f = ex2_approx(ml.x - mn);
+    float ls = f * ml.y;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    l = fmaf(l, fa, ls);
+    m = mn;
+    o.x *= fa, o.y *= fa, o.z *= fa, o.w *= fa;
+    const int n = min(32, J.c_last + 1 - p0);
+    for (int p1 = 0; p1 < n; p1 += 8) {
+      float4 x[8];
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        w[e] = __shfl_sync(0xffffffffu, f, (p1 + e) & 31);
+        const bool in = p1 + e < n && w[e] > 0.f;  // a part that sees nothing of the row left nothing
+        if (!in) w[e] = 0.f;
+        x[e] = in ? *(const float4 *)(P.part_o + place(p0 + p1 + e) * X::kD + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o.x = fmaf(w[e], x[e].x, o.x);
+        o.y = fmaf(w[e], x[e].y, o.y);
+        o.z = fmaf(w[e], x[e].z, o.z);
+        o.w = fmaf(w[e], x[e].w, o.w);
+      }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16 *dst = P.out + (((size_t)r.q.s.q0 + tok) * P.D.Hq + r.g * P.D.G + row % P.D.G) * X::kD + col;
-    *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __nv_bfloat16 *dst = P.out + (((size_t)J.q0 + tok) * P.D.Hq + J.g * P.D.G + row % P.D.G) * X::kD + col;
+  *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 // ---------------------------------------------------------------- host side
@@ -449,6 +486,7 @@ cudaError_t launch_chunks(Launch launch, size_t (*smem_of)(bool, int), const Dim
   P.out = (__nv_bfloat16 *)out;
   P.part_o = (float *)scratch;
   P.part_ml = P.part_o + (size_t)2 * kMaxCtas * X::kTiles * kRows * X::kD;
+  P.jobs = (MergeJob *)(P.part_ml + (size_t)2 * kMaxCtas * X::kTiles * kRows * 2);
   P.status = status;
   P.T = kRows / D.G;
   P.sl2 = D.scale * 1.4426950408889634f;
@@ -470,7 +508,7 @@ cudaError_t launch_chunks(Launch launch, size_t (*smem_of)(bool, int), const Dim
     if (e == cudaSuccess) {
       note_launch();
       e = launch_maybe_pdl(k_paged_merge<X>, dim3(P.C, X::kTiles * kRows / kMergeRows, X::kD / 128),
-                           dim3(kMergeWarps * 32), (size_t)(P.nb + 1) * 8, st, true, P);
+                           dim3(kMergeWarps * 32), 0, st, true, P);
     }
     if (e != cudaSuccess) {
       note_error("paged chunk attention launch", e);
@@ -482,7 +520,7 @@ cudaError_t launch_chunks(Launch launch, size_t (*smem_of)(bool, int), const Dim
 
 template <class X>
 size_t partials_bytes() {
-  return (size_t)2 * kMaxCtas * X::kTiles * kRows * (X::kD + 2) * sizeof(float);
+  return (size_t)2 * kMaxCtas * X::kTiles * kRows * (X::kD + 2) * sizeof(float) + kMaxCtas * sizeof(MergeJob);
 }
 
 }  // namespace

@@ -40,7 +40,7 @@ using namespace sm100;
 constexpr int kTile = 16;    // keys per tile
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxSeqs = 1024;  // sequences per launch (their prefix sums sit in shared memory)
+constexpr int kMaxSeqs = 512;   // sequences per launch (their geometry sits in shared memory)
 constexpr int kMaxCtas = 1024;
 constexpr int kMaxRows = 16;
 
@@ -65,19 +65,28 @@ struct RowsParams {
 };
 
 // ---------------------------------------------------------------- the list of items
+struct SeqItems {
+  int q0, n, len;  // n = 0: nothing to do here
+  int rt, tiles;   // units per KV head, tiles per unit
+};
 struct Plan {
   long long *pre;   // [nb + 1] items before sequence b
-  int *rt, *tiles;  // [nb] units per KV head, tiles per unit
+  SeqItems *seq;    // [nb]
   long long T;
   int C;            // CTAs that take part
 };
+__host__ __device__ constexpr size_t plan_bytes(int nb) { return (size_t)(nb + 1) * 8 + (size_t)nb * sizeof(SeqItems); }
+
+// Divisions here have 64-bit operands that nearly always fit 32 bits, where they are much cheaper.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Every CTA for itself: items per sequence and their prefix sums.
 __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
   __shared__ long long s_sum[kWarps];
   L.pre = (long long *)smem;
-  L.rt = (int *)(smem + (size_t)(P.nb + 1) * 8);
-  L.tiles = L.rt + P.nb;
+  L.seq = (SeqItems *)(smem + (size_t)(P.nb + 1) * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (P.nb + kThreads - 1) / kThreads;
   const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
@@ -95,8 +104,7 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
       rt = (int)(((long long)s.n * P.G + P.R - 1) / P.R);
       tiles = (s.len + kTile - 1) / kTile;
     }
-    L.rt[b] = rt;
-    L.tiles[b] = tiles;
+    L.seq[b] = {s.q0, s.n, s.len, rt, tiles};
     run += (long long)rt * tiles * P.Hkv;
     L.pre[b + 1] = run;
   }
@@ -118,13 +126,13 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
 }
 
 // CTA of item i: floor(c T / C) <= i < floor((c + 1) T / C)
-__device__ __forceinline__ int cta_of(long long i, int C, long long T) { return (int)(((i + 1) * C + T - 1) / T) - 1; }
+__device__ __forceinline__ int cta_of(long long i, int C, long long T) { return (int)div_pos((i + 1) * C + T - 1, T) - 1; }
 
 // A unit: its sequence, KV head and rows, and where its items are in the list.
 struct Unit {
   int b, g, r;           // sequence of the launch, KV head, unit of the sequence and head
   long long first, end;  // items
-  PagedSeq s;
+  SeqItems s;
 };
 
 __device__ __forceinline__ Unit unit_of(const RowsParams &P, const Plan &L, long long i) {
@@ -136,14 +144,12 @@ __device__ __forceinline__ Unit unit_of(const RowsParams &P, const Plan &L, long
   }
   Unit u;
   u.b = lo;
-  const long long local = i - L.pre[lo];
-  const int tiles = L.tiles[lo];
-  const int n = (int)(local / tiles);
-  u.g = n / L.rt[lo];
-  u.r = n % L.rt[lo];
-  u.first = L.pre[lo] + (long long)n * tiles;
-  u.end = u.first + tiles;
-  u.s = paged_seq(P.P, P.b0 + lo, nullptr);
+  u.s = L.seq[lo];
+  const int n = (int)div_pos(i - L.pre[lo], u.s.tiles);
+  u.g = n / u.s.rt;
+  u.r = n % u.s.rt;
+  u.first = L.pre[lo] + (long long)n * u.s.tiles;
+  u.end = u.first + u.s.tiles;
   return u;
 }
 
@@ -210,12 +216,11 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v
 __device__ __forceinline__ float weight_of(float m, float m_max) { return m == -INFINITY ? 0.f : ex2_approx(m - m_max); }
 
 // The CTA's items [i0, i1) of unit u are done: NB buffers buf[w] ([R][d] fp32, swizzled where
-// warps have one each) with their wm / wl hold them. A whole unit is written out; a part goes to the CTA's slot, and
-// the last part's CTA merges the unit. Ends with a barrier.
+// warps have one each) with their wm / wl hold them. A whole unit is written out; a part goes to
+// the CTA's slot. Ends with a barrier.
 template <typename T, int NB>
 __device__ __forceinline__ void finish_segment(const RowsParams &P, const Plan &L, const Unit &u, long long i0, long long i1,
                                                long long lo, float *const (&buf)[NB], const float *wm, const float *wl) {
-  __shared__ int s_last;
   const int d = P.d, R = P.R, d4 = d >> 2;
   const int c = blockIdx.x;
   const bool whole = i0 == u.first && i1 == u.end;
@@ -252,38 +257,56 @@ __device__ __forceinline__ void finish_segment(const RowsParams &P, const Plan &
     }
   }
   __syncthreads();  // the buffers are free; a part is written
-  if (whole) return;
+}
+
+// The CTA's part of unit u, if it is one, is counted, and where the count is complete the unit is
+// merged. At once, not after the CTA's last segment, where it costs 1.5 us more (35.2 against 33.7 at
+// the 64-sequence step over selected blocks): the other CTA of the SM covers it here.
+template <typename T>
+__device__ __forceinline__ void settle(const RowsParams &P, const Plan &L, const Unit &u, long long i0, long long i1) {
+  __shared__ int s_last;
+  if (i0 == u.first && i1 == u.end) return;
+  const int d = P.d, R = P.R, d4 = d >> 2;
   const int c_first = cta_of(u.first, L.C, L.T), n_parts = cta_of(u.end - 1, L.C, L.T) - c_first + 1;
   if (threadIdx.x == 0) {
-    // the barrier orders the CTA's partial before this release; the last part acquires them all
+    // the barrier before orders the CTA's partial before this release; the last part acquires them all
     int old;
     asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(old) : "l"(&P.done[c_first]) : "memory");
     s_last = old == n_parts - 1;
   }
   __syncthreads();
   if (s_last) {
-    const int s0 = 2 * c_first + ((long long)c_first * L.T / L.C == u.first ? 0 : 1);
-    auto slot_of = [&](int p) { return p == 0 ? s0 : 2 * (c_first + p); };
+    const int s0 = 2 * c_first + (div_pos((long long)c_first * L.T, L.C) == u.first ? 0 : 1);
     for (int e = threadIdx.x; e < R * d4; e += kThreads) {
       const int r = e / d4, c4 = (e - r * d4) * 4;
       int tok, h;
       if (!unit_row(P, u, r, tok, h)) continue;
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int p = 0; p < n_parts; ++p) {
-        const size_t at = (size_t)slot_of(p) * R + r;
-        const float2 ml = __ldcg((const float2 *)(P.part_ml + at * 2));
-        const float4 x = __ldcg((const float4 *)(P.part_o + at * d + c4));
-        if (ml.x == -INFINITY) continue;  // a part that sees no key of this row
-        const float mn = fmaxf(m, ml.x);
-        const float fa = ex2_approx(m - mn), fb = ex2_approx(ml.x - mn);
-        o.x = fmaf(fb, x.x, o.x * fa);
-        o.y = fmaf(fb, x.y, o.y * fa);
-        o.z = fmaf(fb, x.z, o.z * fa);
-        o.w = fmaf(fb, x.w, o.w * fa);
-        l = fmaf(fb, ml.y, l * fa);
+      for (int p0 = 0; p0 < n_parts; p0 += 4) {  // four parts' loads at once
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int p = p0 + q;
+          const size_t at = (size_t)(p == 0 ? s0 : 2 * (c_first + p)) * R + r;
+          ml[q] = p < n_parts ? __ldcg((const float2 *)(P.part_ml + at * 2)) : make_float2(-INFINITY, 0.f);
+          x[q] = p < n_parts ? __ldcg((const float4 *)(P.part_o + at * d + c4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+        const float fa = weight_of(m, mn);
+        o.x *= fa, o.y *= fa, o.z *= fa, o.w *= fa;
+        l *= fa;
         m = mn;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float f = weight_of(ml[q].x, mn);
+          o.x = fmaf(f, x[q].x, o.x);
+          o.y = fmaf(f, x[q].y, o.y);
+          o.z = fmaf(f, x[q].z, o.z);
+          o.w = fmaf(f, x[q].w, o.w);
+          l = fmaf(f, ml[q].y, l);
+        }
       }
       const bool any = l > 0.f;
       const float inv = any ? 1.f / l : 0.f;
@@ -356,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
   make_plan(P, smem + Y::kOffPlan, L);
   const int c = blockIdx.x;
   if (c >= L.C) return;
-  const long long lo = (long long)c * L.T / L.C, hi = (long long)(c + 1) * L.T / L.C;
+  const long long lo = div_pos((long long)c * L.T, L.C), hi = div_pos((long long)(c + 1) * L.T, L.C);
 
   // ---- this warp's stream: iteration n is item lo + warp + kWarps n
   long long row_l = 0;  // lane l: pool row, first key and key count of iteration 32 (n / 32) + l
@@ -552,6 +575,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
       buf[w] = (float *)(smem + w * Y::kWarpBytes + ((nw + S - 1) % S) * Y::kStageBytes);
     }
     finish_segment<__nv_bfloat16, kWarps>(P, L, u, i0, i1, lo, buf, wm, wl);
+    settle<__nv_bfloat16>(P, L, u, i0, i1);
     i0 = i1;
   }
   cp_wait<0>();
@@ -594,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__
   make_plan(P, smem + fixed, L);
   const int c = blockIdx.x;
   if (c >= L.C) return;
-  const long long lo = (long long)c * L.T / L.C, hi = (long long)(c + 1) * L.T / L.C;
+  const long long lo = div_pos((long long)c * L.T, L.C), hi = div_pos((long long)(c + 1) * L.T, L.C);
   constexpr int kRW = kMaxRows / kWarps;  // rows per warp
 
   for (long long i0 = lo; i0 < hi;) {
@@ -716,6 +740,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__
     }
     float *buf[1] = {os};
     finish_segment<T, 1>(P, L, u, i0, i1, lo, buf, wm, wl);
+    settle<T>(P, L, u, i0, i1);
     i0 = i1;
   }
 }
@@ -734,7 +759,7 @@ int ctas_per_sm(size_t smem) { return std::max(1, std::min(3, (int)(228 * 1024 /
 template <int D, int NT>
 cudaError_t launch_mma(RowsParams &P, cudaStream_t st) {
   typedef MmaLayout<D, NT> Y;
-  const size_t smem = Y::kOffPlan + (size_t)(P.nb + 1) * 16;
+  const size_t smem = Y::kOffPlan + plan_bytes(P.nb);
   P.C = min(sm_count() * ctas_per_sm(smem), kMaxCtas);
   cudaError_t e = ensure_smem(k_paged_rows<D, NT>, smem);
   if (e != cudaSuccess) return e;
@@ -746,7 +771,7 @@ cudaError_t launch_mma(RowsParams &P, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_simt(RowsParams &P, cudaStream_t st) {
   const size_t fixed = (simt_fixed_bytes(P.d) + 15) & ~(size_t)15;
-  const size_t smem = fixed + (size_t)(P.nb + 1) * 16;
+  const size_t smem = fixed + plan_bytes(P.nb);
   P.C = min(sm_count() * ctas_per_sm(smem), kMaxCtas);
   cudaError_t e = ensure_smem(k_paged_simt<T>, smem);
   if (e != cudaSuccess) return e;

@@ -67,7 +67,8 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   uint64_t *bars = (uint64_t *)(base + kOffBar);
   uint32_t *tmem_slot = (uint32_t *)(base + kOffMisc);
   volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
-  long long *pre = (long long *)(base + kOffBits + (kSel ? 2 * kBitSlotBytes : 0));
+  uint8_t *plan = base + kOffBits + (kSel ? 2 * kBitSlotBytes : 0);
+  const PlanArea L = {(long long *)plan, (SeqGeo *)(plan + (size_t)(P.nb + 1) * 8)};
 
   const Dims &D = P.D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -94,7 +95,7 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  make_plan<One256>(P, pre, blockIdx.x == 0 ? P.status : nullptr);
+  make_plan<One256>(P, L, blockIdx.x == 0 ? P.status : nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -102,7 +103,7 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
   if (warp == kBuilderWarp) {
     const SlotArea area = {&bars[kBarSlotFull], &bars[kBarSlotFree], base + kOffInfo, base + kOffBits, abort_flag};
-    build_segments<One256, kSel>(P, area, pre, lane);
+    build_segments<One256, kSel>(P, area, L, lane);
   } else if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     // Lane 4 i + e < 4 * 64 / box holds the pool plane (page, KV head) of the i-th box of the next
@@ -450,8 +451,8 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   }
 }
 
-size_t smem_of(bool sel, int nb) { return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + (size_t)(nb + 1) * 8; }
-static_assert(1024 + kOffBits + 2 * kBitSlotBytes + (kMaxSeqs + 1) * 8 <= 227 * 1024, "shared memory");
+size_t smem_of(bool sel, int nb) { return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + plan_bytes(nb); }
+static_assert(1024 + kOffBits + 2 * kBitSlotBytes + plan_bytes(kMaxSeqs) <= 227 * 1024, "shared memory");
 
 }  // namespace
 
