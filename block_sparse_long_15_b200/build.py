@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libqsa.so")
 LIB_DEBUG = os.path.join(PKG, "libqsa_debug.so")
 SOURCES = ["qsa_api.cu", "qsa_simt.cu", "qsa_score_tc.cu", "qsa_attn_tc.cu", "qsa_attn_tc1.cu", "qsa_decode.cu",
            "qsa_offload.cu", "qsa_selftest.cu", "qsa_proj.cu", "qsa_check.cu", "qsa_paged_cache.cu", "qsa_paged_rows.cu",
-           "qsa_paged_tc.cu", "qsa_paged_tc256.cu"]
+           "qsa_paged_tc.cu", "qsa_paged_tc1.cu"]
 DEBUG_SOURCES = ["qsa_api.cu"]  # recompiled with -DQSA_DEBUG for libqsa_debug.so
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -265,9 +265,9 @@ bool paged_tc_supported(const Dims &D, const Paged &P, bool sel);
 size_t paged_tc_workspace(const Dims &D);
 cudaError_t launch_paged_tc(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st);
-// The head_dim 256 form of launch_paged_tc.
-size_t paged_tc256_workspace();
-cudaError_t launch_paged_tc256(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
-                               const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st);
+// The one-tile form of launch_paged_tc (head_dim 128 and 256).
+size_t paged_tc1_workspace(const Dims &D);
+cudaError_t launch_paged_tc1(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
+                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st);
 
 }  // namespace qsa

@@ -561,11 +561,14 @@ bool paged_tc_supported(const Dims &D, const Paged &G, bool sel) {
          (long long)G.n_pages * D.Hkv <= 0x7fffffffLL;
 }
 
-size_t paged_tc_workspace(const Dims &D) { return D.d == 256 ? paged_tc256_workspace() : partials_bytes<Two128>(); }
+// The one-tile kernel takes less.
+size_t paged_tc_workspace(const Dims &D) { return D.d == 256 ? paged_tc1_workspace(D) : partials_bytes<Two128>(); }
 
 cudaError_t launch_paged_tc(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
-  if (D.d == 256) return launch_paged_tc256(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+  // Sequences whose rows fill no more than one tile leave the second one idle.
+  if (D.d == 256 || (long long)G.max_chunk * D.G <= kRows)
+    return launch_paged_tc1(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
   CUtensorMap tq;
   if (!encode_fn() || !make_map(&tq, q, kD, D.Hq, G.n_tok, D.G, kRows / D.G)) {
     note_error("paged attention tensor maps", cudaErrorInvalidValue);

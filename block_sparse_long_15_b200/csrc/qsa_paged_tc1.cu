@@ -1,87 +1,97 @@
 // Attention of chunks of new tokens over a paged K/V cache on 5th-generation tensor cores
-// (tcgen05), head_dim 256: see qsa_paged_tc.cu for head_dim 128 and qsa_paged_plan.cuh for how
-// the work is divided.
+// (tcgen05), one 128-row tile per CTA: head_dim 256, and head_dim 128 for sequences of no more
+// than 128 (token, head) rows. See qsa_paged_tc.cu for head_dim 128 otherwise and
+// qsa_paged_plan.cuh for how the work is divided.
 //
-// O of one 128-row tile takes 256 TMEM columns, so a CTA holds one tile: T = 128 / G tokens of
-// one KV head against 64-key chunks, 1024 clocks of products and 512 of exponentials each.
-// Q sits in TMEM too (128 columns): the QK product then reads only K from shared memory, at
-// half the rate that its 64 columns would need with both operands there, and shared memory is
-// left to six 32 KB stages of K and V. S is double-buffered, so the softmax of a chunk runs
-// beside the products of its neighbours:
-//   warp 0      TMA producer: K and V of a chunk into two 3-deep rings; 4 lanes per page box,
-//               one for each 64 columns;
+// At head_dim 256 O of one tile takes 256 TMEM columns, so a CTA holds T = 128 / G tokens of one
+// KV head against 64-key chunks, 1024 clocks of products and 512 of exponentials each. With few
+// rows (drafted tokens) K and V are read for one tile anyway, and the call is bound by HBM.
+// Q sits in TMEM too: the QK product then reads only K from shared memory, at half the rate that
+// its 64 columns would need with both operands there, and shared memory is left to 192 KB of K and
+// V stages. S is double-buffered, so the softmax of a chunk runs beside the products of its
+// neighbours:
+//   warp 0      TMA producer: K and V of a chunk into two rings, 3 deep (6 at head_dim 128); one
+//               lane per page box and 64 columns;
 //   warp 1      MMA issuer (TMEM owner): O += P(n) V, S = Q K(n + 2)^T into the buffer that
 //               P(n) has just left;
 //   warp 2      builder;
 //   warps 4-11  softmax, 16 rows per warp, two threads a row with 32 logits each, Q of the next
 //               unit into TMEM, and the epilogue.
-// TMEM: O at 0, Q at 256, S (then P, in its first half) at 384 and 448.
+// TMEM: O, then Q, then two buffers of S (then P, in its first half).
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
 #include "qsa_paged_plan.cuh"
 
 namespace qsa {
 namespace {
 
-struct One256 {
-  static constexpr int kD = 256, kTiles = 1, kChunk = 64;
+constexpr int kChunk = 64;  // keys per chunk
+template <int D_>
+struct One {
+  static constexpr int kD = D_, kTiles = 1, kChunk = qsa::kChunk;
 };
-constexpr int kD = One256::kD, kChunk = One256::kChunk;
-constexpr int kNR = 3;  // depth of each ring
 constexpr int kThreads = 384;
 constexpr int kBuilderWarp = 2;
 constexpr int kSoftWarp0 = 4;
 constexpr int kSoftWarps = 8;
-constexpr uint32_t kTmemCols = 512, kColQ = 256, kColS = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kGroupBytes = kChunk * 128;  // 64 columns of a chunk's rows
 
-constexpr uint32_t kStageBytes = kChunk * kD * 2;   // 4 groups of [64 rows][128 B]
-constexpr uint32_t kGroupBytes = kChunk * 128;
-constexpr uint32_t kOffK = 0;
-constexpr uint32_t kOffV = kOffK + kNR * kStageBytes;
-constexpr uint32_t kOffBar = kOffV + kNR * kStageBytes;
-constexpr uint32_t kOffMisc = kOffBar + 256;
-constexpr uint32_t kOffInfo = kOffMisc + 64;
-constexpr uint32_t kOffBits = kOffInfo + 2 * kInfoBytes;
+template <int D_>
+struct Layout {
+  static constexpr int kNR = D_ == 256 ? 3 : 6;      // depth of each ring
+  static constexpr int kGroups = D_ / 64;
+  static constexpr uint32_t kStageBytes = kChunk * D_ * 2;
+  static constexpr uint32_t kColQ = D_, kColS = D_ + D_ / 2;
+  static constexpr uint32_t kOffK = 0;
+  static constexpr uint32_t kOffV = kOffK + kNR * kStageBytes;
+  static constexpr uint32_t kOffBar = kOffV + kNR * kStageBytes;
+  static constexpr uint32_t kOffMisc = kOffBar + 512;
+  static constexpr uint32_t kOffInfo = kOffMisc + 64;
+  static constexpr uint32_t kOffBits = kOffInfo + 2 * kInfoBytes;
+  // barrier slots
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarKEmpty = kBarKFull + kNR;
+  static constexpr int kBarVFull = kBarKEmpty + kNR;
+  static constexpr int kBarVEmpty = kBarVFull + kNR;
+  static constexpr int kBarSFull = kBarVEmpty + kNR;     // [S buffer]
+  static constexpr int kBarPFull = kBarSFull + 2;        // [S buffer], 8 arrivals
+  static constexpr int kBarPVDone = kBarPFull + 2;       // a phase per PV
+  static constexpr int kBarODone = kBarPVDone + 1;       // a phase per unit: its last PV completed
+  static constexpr int kBarQFull = kBarODone + 1;        // a phase per unit: Q is in TMEM, 8 arrivals
+  static constexpr int kBarQEmpty = kBarQFull + 1;       // a phase per unit: its last QK completed
+  static constexpr int kBarSlotFull = kBarQEmpty + 1;    // [slot], the builder's 32 lanes
+  static constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
+  static constexpr int kNumBars = kBarSlotFree + 2;
+  static_assert(kNumBars * 8 <= 512, "barrier area");
+};
 
-// barrier slots
-constexpr int kBarKFull = 0;
-constexpr int kBarKEmpty = kBarKFull + kNR;
-constexpr int kBarVFull = kBarKEmpty + kNR;
-constexpr int kBarVEmpty = kBarVFull + kNR;
-constexpr int kBarSFull = kBarVEmpty + kNR;     // [S buffer]
-constexpr int kBarPFull = kBarSFull + 2;        // [S buffer], 8 arrivals
-constexpr int kBarPVDone = kBarPFull + 2;       // a phase per PV
-constexpr int kBarODone = kBarPVDone + 1;       // a phase per unit: its last PV completed
-constexpr int kBarQFull = kBarODone + 1;        // a phase per unit: Q is in TMEM, 8 arrivals
-constexpr int kBarQEmpty = kBarQFull + 1;       // a phase per unit: its last QK completed
-constexpr int kBarSlotFull = kBarQEmpty + 1;    // [slot], the builder's 32 lanes
-constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
-constexpr int kNumBars = kBarSlotFree + 2;
-static_assert(kNumBars * 8 <= 256, "barrier area");
-
-template <bool kSel>
+template <int D_, bool kSel>
 __global__ void __launch_bounds__(kThreads, 1)
-k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ TcParams P) {
+k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            const __grid_constant__ TcParams P) {
+  typedef One<D_> X;
+  typedef Layout<D_> Y;
+  constexpr int kD = D_, kNR = Y::kNR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t *bars = (uint64_t *)(base + kOffBar);
-  uint32_t *tmem_slot = (uint32_t *)(base + kOffMisc);
-  volatile int *abort_flag = (volatile int *)(base + kOffMisc + 8);
-  uint8_t *plan = base + kOffBits + (kSel ? 2 * kBitSlotBytes : 0);
+  uint64_t *bars = (uint64_t *)(base + Y::kOffBar);
+  uint32_t *tmem_slot = (uint32_t *)(base + Y::kOffMisc);
+  volatile int *abort_flag = (volatile int *)(base + Y::kOffMisc + 8);
+  uint8_t *plan = base + Y::kOffBits + (kSel ? 2 * kBitSlotBytes : 0);
   const PlanArea L = {(long long *)plan, (SeqGeo *)(plan + (size_t)(P.nb + 1) * 8)};
 
   const Dims &D = P.D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = P.T, G = D.G;
-  auto info = [&](int s) { return (const UnitInfo *)(base + kOffInfo + s * kInfoBytes); };
-  auto token_bits = [&](int s) { return (const uint32_t *)(base + kOffBits + s * kBitSlotBytes); };
+  auto info = [&](int s) { return (const UnitInfo *)(base + Y::kOffInfo + s * kInfoBytes); };
+  auto token_bits = [&](int s) { return (const uint32_t *)(base + Y::kOffBits + s * kBitSlotBytes); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
+    for (int i = 0; i < Y::kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kBarPFull || i == kBarPFull + 1 || i == kBarQFull) count = kSoftWarps;
-      if (i == kBarSlotFull || i == kBarSlotFull + 1) count = 32;
-      if (i == kBarSlotFree || i == kBarSlotFree + 1) count = 2 + kSoftWarps;
+      if (i == Y::kBarPFull || i == Y::kBarPFull + 1 || i == Y::kBarQFull) count = kSoftWarps;
+      if (i == Y::kBarSlotFull || i == Y::kBarSlotFull + 1) count = 32;
+      if (i == Y::kBarSlotFree || i == Y::kBarSlotFree + 1) count = 2 + kSoftWarps;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
@@ -95,32 +105,32 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  make_plan<One256>(P, L, blockIdx.x == 0 ? P.status : nullptr);
+  make_plan<X>(P, L, blockIdx.x == 0 ? P.status : nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
   if (warp == kBuilderWarp) {
-    const SlotArea area = {&bars[kBarSlotFull], &bars[kBarSlotFree], base + kOffInfo, base + kOffBits, abort_flag};
-    build_segments<One256, kSel>(P, area, L, lane);
+    const SlotArea area = {&bars[Y::kBarSlotFull], &bars[Y::kBarSlotFree], base + Y::kOffInfo, base + Y::kOffBits, abort_flag};
+    build_segments<X, kSel>(P, area, L, lane);
   } else if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    // Lane 4 i + e < 4 * 64 / box holds the pool plane (page, KV head) of the i-th box of the next
-    // chunk (-1: no token there, or a page outside the pool) and loads its columns 64 e ..
-    const int n_lanes = 4 * (kChunk / P.box), box_i = lane >> 2, e = lane & 3;
+    // Lane i * groups + e holds the pool plane (page, KV head) of the i-th box of the next chunk (-1:
+    // no token there, or a page outside the pool) and loads its columns 64 e ..
+    const int n_lanes = Y::kGroups * (kChunk / P.box), box_i = lane / Y::kGroups, e = lane % Y::kGroups;
     const uint32_t box_bytes = (uint32_t)P.box * 128;
     int j = 0;  // chunks so far
     bool fail = false;
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
-      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+      if (!idle_wait_warp(&bars[Y::kBarSlotFull + s], (su >> 1) & 1)) {
         fail = true;
         break;
       }
       const UnitInfo I = *info(s);
       if (!I.live) break;
-      const Chunks<One256, kSel> ch(I, token_bits(s) + kBitWords, P.W);
+      const Chunks<X, kSel> ch(I, token_bits(s) + kBitWords, P.W);
       const int t_hi = I.len - I.n + min(I.n, I.r0 + T) - 1;  // the unit's last visible key
       auto plane = [&](int c) {
         int z = -1;
@@ -138,28 +148,28 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int cn = ch.next(c + 1), zn = plane(cn);  // read ahead
         const int st = j % kNR, y = (c * kChunk + box_i * P.box) & (P.P.ps - 1);
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, z >= 0)) * box_bytes;
-        const uint32_t at = st * kStageBytes + e * kGroupBytes + box_i * box_bytes;
-        if (j >= kNR && !warp_wait(&bars[kBarKEmpty + st], ((j / kNR) & 1) ^ 1)) {
+        const uint32_t at = st * Y::kStageBytes + e * kGroupBytes + box_i * box_bytes;
+        if (j >= kNR && !warp_wait(&bars[Y::kBarKEmpty + st], ((j / kNR) & 1) ^ 1)) {
           fail = true;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kBarKFull + st], bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[Y::kBarKFull + st], bytes);
         __syncwarp();
-        if (z >= 0) tma_load_3d(&tm_k, &bars[kBarKFull + st], base + kOffK + at, e * 64, y, z);
-        if (j >= kNR && !warp_wait(&bars[kBarVEmpty + st], ((j / kNR) & 1) ^ 1)) {
+        if (z >= 0) tma_load_3d(&tm_k, &bars[Y::kBarKFull + st], base + Y::kOffK + at, e * 64, y, z);
+        if (j >= kNR && !warp_wait(&bars[Y::kBarVEmpty + st], ((j / kNR) & 1) ^ 1)) {
           fail = true;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kBarVFull + st], bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[Y::kBarVFull + st], bytes);
         __syncwarp();
-        if (z >= 0) tma_load_3d(&tm_v, &bars[kBarVFull + st], base + kOffV + at, e * 64, y, z);
+        if (z >= 0) tma_load_3d(&tm_v, &bars[Y::kBarVFull + st], base + Y::kOffV + at, e * 64, y, z);
         __syncwarp();
         c = cn;
         z = zn;
         ++j;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+      if (lane == 0) mbar_arrive(&bars[Y::kBarSlotFree + s]);
     }
     if (fail) {
       if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
@@ -169,40 +179,40 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kChunk, false, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, kD, false, true);
-    const uint64_t k_desc0 = sdesc_sw128(smem_u32(base + kOffK), 16, 1024);
-    const uint64_t v_desc0 = sdesc_sw128(smem_u32(base + kOffV), kGroupBytes, 1024);
+    const uint64_t k_desc0 = sdesc_sw128(smem_u32(base + Y::kOffK), 16, 1024);
+    const uint64_t v_desc0 = sdesc_sw128(smem_u32(base + Y::kOffV), kGroupBytes, 1024);
     int nk = 0, nv = 0;  // QKs and PVs so far, over all units
     int units = 0;
     bool fail = false, first = true;  // the unit's next PV overwrites O
     auto issue_qk = [&]() -> bool {   // S(nk) = Q K(nk)^T into S buffer nk % 2
       const int st = nk % kNR;
-      if (!warp_wait(&bars[kBarKFull + st], (nk / kNR) & 1)) return false;
+      if (!warp_wait(&bars[Y::kBarKFull + st], (nk / kNR) & 1)) return false;
       tc_fence_after();
-      const uint64_t kd = k_desc0 + (uint64_t)((st * kStageBytes) >> 4);
-      const uint32_t d = tbase + kColS + (nk & 1) * kChunk;
+      const uint64_t kd = k_desc0 + (uint64_t)((st * Y::kStageBytes) >> 4);
+      const uint32_t d = tbase + Y::kColS + (nk & 1) * kChunk;
 #pragma unroll
       for (int kk = 0; kk < kD / 16; ++kk)
-        mma_ts_w(d, tbase + kColQ + kk * 8, kd + (uint64_t)(((kk >> 2) * kGroupBytes + (kk & 3) * 32) >> 4), idesc_qk,
+        mma_ts_w(d, tbase + Y::kColQ + kk * 8, kd + (uint64_t)(((kk >> 2) * kGroupBytes + (kk & 3) * 32) >> 4), idesc_qk,
                  kk > 0 ? 1u : 0u);
-      mma_commit_w(&bars[kBarSFull + (nk & 1)]);
-      mma_commit_w(&bars[kBarKEmpty + st]);
+      mma_commit_w(&bars[Y::kBarSFull + (nk & 1)]);
+      mma_commit_w(&bars[Y::kBarKEmpty + st]);
       ++nk;
       return true;
     };
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
-      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+      if (!idle_wait_warp(&bars[Y::kBarSlotFull + s], (su >> 1) & 1)) {
         fail = true;
         break;
       }
       const UnitInfo *I = info(s);
       const int live = I->live, part = I->part;
       if (!live) break;
-      const Chunks<One256, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      const Chunks<X, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
       const int t_hi = I->len - I->n + min(I->n, I->r0 + T) - 1;
       if (part & 1) {
         first = true;
-        if (!warp_wait(&bars[kBarQFull], units & 1)) {
+        if (!warp_wait(&bars[Y::kBarQFull], units & 1)) {
           fail = true;
           break;
         }
@@ -216,7 +226,7 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (ca < 0 || !issue_qk()) return ca < 0;
         ca = ch.next(ca + 1);
         if (ca < 0 && (part & 2)) {
-          mma_commit_w(&bars[kBarQEmpty]);
+          mma_commit_w(&bars[Y::kBarQEmpty]);
           q_done = true;
         }
         return true;
@@ -224,8 +234,8 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (!advance_qk() || !advance_qk()) fail = true;
       for (; c >= 0 && !fail; c = ch.next(c + 1)) {
         const int st = nv % kNR;
-        if (!warp_wait(&bars[kBarVFull + st], (nv / kNR) & 1) ||
-            !warp_wait(&bars[kBarPFull + (nv & 1)], (nv >> 1) & 1)) {
+        if (!warp_wait(&bars[Y::kBarVFull + st], (nv / kNR) & 1) ||
+            !warp_wait(&bars[Y::kBarPFull + (nv & 1)], (nv >> 1) & 1)) {
           fail = true;
           break;
         }
@@ -234,9 +244,9 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         // what an unloaded box left) may hold NaN, and 0 * NaN is NaN.
         const int valid_rows = t_hi + 1 - c * kChunk;
         if (valid_rows < kChunk) {
-          uint8_t *vs = base + kOffV + st * kStageBytes;
+          uint8_t *vs = base + Y::kOffV + st * Y::kStageBytes;
           for (int rr = max(valid_rows, 0) + lane; rr < kChunk; rr += 32)
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < Y::kGroups; ++q) {
               uint4 *p4 = (uint4 *)(vs + q * kGroupBytes + rr * 128);
 #pragma unroll
               for (int x = 0; x < 8; ++x) p4[x] = make_uint4(0, 0, 0, 0);
@@ -244,24 +254,24 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint64_t vd = v_desc0 + (uint64_t)((st * kStageBytes) >> 4);
-        const uint32_t pcol = tbase + kColS + (nv & 1) * kChunk;
+        const uint64_t vd = v_desc0 + (uint64_t)((st * Y::kStageBytes) >> 4);
+        const uint32_t pcol = tbase + Y::kColS + (nv & 1) * kChunk;
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
           mma_ts_w(tbase, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
         first = false;
-        mma_commit_w(&bars[kBarVEmpty + st]);
-        mma_commit_w(&bars[kBarPVDone]);
+        mma_commit_w(&bars[Y::kBarVEmpty + st]);
+        mma_commit_w(&bars[Y::kBarPVDone]);
         ++nv;
         // S of two chunks on goes into the buffer that this PV reads; MMAs run in issue order
         if (!advance_qk()) fail = true;
       }
       if (!fail && (part & 2)) {
-        if (!q_done) mma_commit_w(&bars[kBarQEmpty]);
-        mma_commit_w(&bars[kBarODone]);
+        if (!q_done) mma_commit_w(&bars[Y::kBarQEmpty]);
+        mma_commit_w(&bars[Y::kBarODone]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+      if (lane == 0) mbar_arrive(&bars[Y::kBarSlotFree + s]);
     }
     if (fail && lane == 0) {
       record_status(P.status, QSA_ERR_TIMEOUT);
@@ -270,7 +280,7 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------- softmax + epilogue
     // Warp (lane group, sub-group) owns 16 rows: thread t < 16 holds its row's first 32 keys of every
-    // chunk, dims 0 .. 127 of its Q and columns 0 .. 127 of its O, thread t + 16 the others.
+    // chunk, the first half of its Q and of its O, thread t + 16 the others.
     const int row0 = 32 * (warp & 3) + 16 * ((warp - kSoftWarp0) >> 2);
     const int hh = lane >> 4, row = row0 + (lane & 15);
     const int tok = row / G, h = row % G;
@@ -282,7 +292,7 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     bool fail = false;
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
-      if (!idle_wait_warp(&bars[kBarSlotFull + s], (su >> 1) & 1)) {
+      if (!idle_wait_warp(&bars[Y::kBarSlotFull + s], (su >> 1) & 1)) {
         fail = true;
         break;
       }
@@ -292,34 +302,35 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int t0 = I->len - I->n + I->r0;  // the unit's first position
       const bool valid = tok < T && I->r0 + tok < I->n;
       const int t = valid ? t0 + tok : -1;
-      const size_t at = (((size_t)I->q0 + (valid ? I->r0 + tok : 0)) * D.Hq + I->g * G + h) * kD + hh * 128;
+      const size_t at = (((size_t)I->q0 + (valid ? I->r0 + tok : 0)) * D.Hq + I->g * G + h) * kD + hh * (kD / 2);
       if (part_of & 1) {
         some = false;
         m_ref = -INFINITY;
         l = 0.f;
         // Q of the unit, once every QK of the unit before has completed
-        uint32_t q0[32], q1[32];
+        constexpr int kQ = kD / 128;  // 64 dims at a time
+        uint32_t q[kQ][32];
         const uint4 *src = (const uint4 *)(P.q + at);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 a = valid ? src[i] : make_uint4(0, 0, 0, 0), b = valid ? src[i + 8] : make_uint4(0, 0, 0, 0);
-          q0[4 * i] = a.x, q0[4 * i + 1] = a.y, q0[4 * i + 2] = a.z, q0[4 * i + 3] = a.w;
-          q1[4 * i] = b.x, q1[4 * i + 1] = b.y, q1[4 * i + 2] = b.z, q1[4 * i + 3] = b.w;
+        for (int i = 0; i < 8 * kQ; ++i) {
+          const uint4 x = valid ? src[i] : make_uint4(0, 0, 0, 0);
+          uint32_t *d = &q[i / 8][4 * (i % 8)];
+          d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
         }
-        if (units > 0 && !warp_wait(&bars[kBarQEmpty], (units - 1) & 1)) {
+        if (units > 0 && !warp_wait(&bars[Y::kBarQEmpty], (units - 1) & 1)) {
           fail = true;
           break;
         }
         tc_fence_after();
-        tmem_st32_split<64>(lane_addr + kColQ, q0);
-        tmem_st32_split<64>(lane_addr + kColQ + 32, q1);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) tmem_st32_split<kD / 4>(lane_addr + Y::kColQ + 32 * i, q[i]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarQFull]);
+        if (lane == 0) mbar_arrive(&bars[Y::kBarQFull]);
         ++units;
       }
-      const Chunks<One256, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
+      const Chunks<X, kSel> ch(*I, token_bits(s) + kBitWords, P.W);
       // A chunk whose last key is no further than t_free needs no mask per key: without a selection
       // the position of the warp's first row, with one the unit's last visible key.
       const int t_free = kSel ? t0 + min(I->n - I->r0, T) - 1 : t0 + row0 / G;
@@ -334,8 +345,8 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           part = part || __any_sync(0xffffffffu, lim > 0 && lim < 32);
           any = __any_sync(0xffffffffu, lim > 0);
         }
-        const uint32_t s_col = lane_addr + kColS + (n_all & 1) * kChunk;
-        if (!warp_wait(&bars[kBarSFull + (n_all & 1)], (n_all >> 1) & 1)) {
+        const uint32_t s_col = lane_addr + Y::kColS + (n_all & 1) * kChunk;
+        if (!warp_wait(&bars[Y::kBarSFull + (n_all & 1)], (n_all >> 1) & 1)) {
           fail = true;
           break;
         }
@@ -364,19 +375,19 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           // A row that had a reference had a chunk before. S of this chunk being there proves the PV
           // before the last complete, so one parity wait covers the last; the next one waits for
           // this warp's arrival below.
-          if (!warp_wait(&bars[kBarPVDone], (n_all - 1) & 1)) {
+          if (!warp_wait(&bars[Y::kBarPVDone], (n_all - 1) & 1)) {
             fail = true;
             break;
           }
           tc_fence_after();
 #pragma unroll 1
-          for (int cb = 0; cb < 4; ++cb) {
+          for (int cb = 0; cb < kD / 64; ++cb) {
             uint32_t ov[32];
-            tmem_ld32_split<128>(lane_addr + cb * 32, ov);
+            tmem_ld32_split<kD / 2>(lane_addr + cb * 32, ov);
             tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
-            tmem_st32_split<128>(lane_addr + cb * 32, ov);
+            tmem_st32_split<kD / 2>(lane_addr + cb * 32, ov);
           }
           l *= alpha;
         }
@@ -396,14 +407,14 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarPFull + (n_all & 1)]);
+        if (lane == 0) mbar_arrive(&bars[Y::kBarPFull + (n_all & 1)]);
         some = true;
         ++n_all;
       }
       if ((part_of & 2) || fail) {
         const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);  // the row's sum over both key ranges
         // ------------------------------------------------------------ epilogue
-        const bool have_o = !fail && warp_wait(&bars[kBarODone], (units - 1) & 1) && some;
+        const bool have_o = !fail && warp_wait(&bars[Y::kBarODone], (units - 1) & 1) && some;
         if (!have_o && some && !fail) fail = true;
         if (fail) {
           if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
@@ -417,11 +428,11 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (slot >= 0 && valid && hh == 0)
           *(float2 *)(P.part_ml + pr * 2) = make_float2(keep ? m_ref : -INFINITY, keep ? lt : 0.f);
 #pragma unroll 1
-        for (int cb = 0; cb < 8; ++cb) {
+        for (int cb = 0; cb < kD / 32; ++cb) {
           uint32_t ov[16];
           __syncwarp();
           if (have_o) {  // the same for the whole warp
-            tmem_ld16_split<128>(lane_addr + cb * 16, ov);
+            tmem_ld16_split<kD / 2>(lane_addr + cb * 16, ov);
             tmem_ld_wait();
           }
           if (valid && slot < 0) {
@@ -433,14 +444,14 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           } else if (valid && have_o) {
-            uint4 *o4 = (uint4 *)(P.part_o + pr * kD + hh * 128 + cb * 16);
+            uint4 *o4 = (uint4 *)(P.part_o + pr * kD + hh * (kD / 2) + cb * 16);
 #pragma unroll
             for (int q = 0; q < 4; ++q) o4[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarSlotFree + s]);
+      if (lane == 0) mbar_arrive(&bars[Y::kBarSlotFree + s]);
     }
   }
   tc_fence_before();
@@ -451,21 +462,34 @@ k_paged_tc256(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   }
 }
 
-size_t smem_of(bool sel, int nb) { return 1024 + kOffBits + (sel ? 2 * kBitSlotBytes : 0) + plan_bytes(nb); }
-static_assert(1024 + kOffBits + 2 * kBitSlotBytes + plan_bytes(kMaxSeqs) <= 227 * 1024, "shared memory");
+template <int D_>
+size_t smem_of(bool sel, int nb) {
+  return 1024 + Layout<D_>::kOffBits + (sel ? 2 * kBitSlotBytes : 0) + plan_bytes(nb);
+}
+static_assert(1024 + Layout<256>::kOffBits + 2 * kBitSlotBytes + plan_bytes(kMaxSeqs) <= 227 * 1024, "shared memory");
+static_assert(1024 + Layout<128>::kOffBits + 2 * kBitSlotBytes + plan_bytes(kMaxSeqs) <= 227 * 1024, "shared memory");
 
-}  // namespace
-
-size_t paged_tc256_workspace() { return partials_bytes<One256>(); }
-
-cudaError_t launch_paged_tc256(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
-                               const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
-  auto kern = sel ? k_paged_tc256<true> : k_paged_tc256<false>;
+template <int D_>
+cudaError_t launch_d(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
+                     const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
+  auto kern = sel ? k_paged_tc1<D_, true> : k_paged_tc1<D_, false>;
   auto launch = [&](const TcParams &P, const CUtensorMap &tk, const CUtensorMap &tv, size_t smem) {
     const cudaError_t e = ensure_smem(kern, smem);
     return e == cudaSuccess ? launch_maybe_pdl(kern, dim3(P.C), dim3(kThreads), smem, st, false, tk, tv, P) : e;
   };
-  return launch_chunks<One256>(launch, smem_of, D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+  return launch_chunks<One<D_>>(launch, smem_of<D_>, D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+}
+
+}  // namespace
+
+size_t paged_tc1_workspace(const Dims &D) {
+  return D.d == 256 ? partials_bytes<One<256>>() : partials_bytes<One<128>>();
+}
+
+cudaError_t launch_paged_tc1(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
+                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
+  return D.d == 256 ? launch_d<256>(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st)
+                    : launch_d<128>(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
 }
 
 }  // namespace qsa

@@ -164,6 +164,16 @@ CASES = [
     ("bf16", 24, 8, 128, 32, 64, 0, [150, 3, 0, 44], [150, 300, 10, 600]),
     ("bf16", 24, 8, 128, 32, 64, 3, [150, 3, 0, 44], [150, 300, 10, 600]),
     ("bf16", 4, 4, 128, 256, 128, 2, [200, 20], [600, 20]),
+    # no more rows than one tile, split over many CTAs
+    ("bf16", 16, 2, 128, 64, 64, 0, [16, 2, 9, 0], [6000, 700, 9, 50]),
+    ("bf16", 16, 2, 128, 16, 64, 5, [16, 2, 9, 0], [6000, 700, 9, 50]),
+    ("bf16", 24, 8, 128, 256, 64, 0, [42, 7], [3000, 2000]),
+    ("bf16", 32, 1, 256, 32, 64, 0, [4, 1, 3], [5000, 1, 700]),
+    ("bf16", 16, 2, 256, 16, 128, 3, [12, 8], [5000, 2300]),
+    # many rows and many parts
+    ("bf16", 16, 2, 128, 32, 64, 0, [300, 40], [4100, 40]),
+    ("bf16", 16, 2, 128, 128, 192, 6, [300, 40], [4100, 2100]),
+    ("bf16", 4, 4, 256, 64, 256, 2, [200, 20], [2600, 1020]),
     ("fp32", 4, 1, 64, 16, 32, 4, [30, 1, 0, 7], [200, 300, 4, 7]),
     ("fp32", 4, 1, 64, 16, 32, 0, [30, 1, 0, 7], [200, 300, 4, 7]),
     ("fp32", 8, 2, 256, 64, 48, 2, [1, 5], [300, 90]),
@@ -203,7 +213,7 @@ def _oracle(s, case):
                        None if s["sel"] is None else s["sel"][r])
 
 
-@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c[:7]) + f"-q{max(c[7])}")
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c[:7]) + f"-q{max(c[7])}-kv{max(c[8])}")
 def test_attention(cuda_lib, case):
     qsa = cuda_lib
     s = _run(qsa, case)
