@@ -534,10 +534,18 @@ qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRop
   return QSA_OK;
 }
 
-// A sequence with this many (token, head) rows goes to the tensor-core kernel.
-int chunk_rows(const Dims &D, bool sel) { return sel ? 64 : D.d == 256 ? 9 : 17; }
+// A sequence with this many (token, head) rows goes to a tensor-core kernel. Without a selection,
+// the row kernel takes units of 16 rows: it is ahead up to there (two drafted tokens of 16
+// sequences at head_dim 128: 55 us against 70; at head_dim 256, where 16 rows leave it one warp a
+// scheduler, 104 against 91).
+int chunk_rows(const Dims &D, bool sel) { return sel ? 12 * D.G : D.d == 256 ? 9 : 17; }
+// With one, it reads every token's own blocks, while a tile reads the union of its tokens': with
+// independent selections of 2048 keys and 2 KV heads of 128 the row kernel takes 41 us for 4 chunks
+// of 32 tokens, 120 for 16 and 233 for 32, the tensor-core kernel 64, 102 and 144; 32 chunks of 8
+// tokens 75 and 130.
 bool use_paged_tc(const Dims &D, const Paged &G, bool sel) {
-  return (long long)G.max_chunk * D.G >= chunk_rows(D, sel) && paged_tc_supported(D, G, sel);
+  if ((long long)G.max_chunk * D.G < chunk_rows(D, sel) || !paged_tc_supported(D, G, sel)) return false;
+  return !sel || (long long)G.n_tok * D.Hkv * D.d * D.k * D.B >= 1LL << 28;
 }
 // The workspace serves both forms of the call.
 size_t paged_scratch(const Dims &D, const Paged &G) {
@@ -653,14 +661,15 @@ qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, cons
   // Sequences with many (token, head) rows go to the tensor-core kernel where it serves the shape,
   // the others to the row kernel; a single sequence to one of them.
   long long rows_below = 1LL << 62;
-  if (use_paged_tc(D, G, sel != nullptr)) {
+  const bool tc = use_paged_tc(D, G, sel != nullptr);
+  if (tc) {
     const int from = G.batch == 1 ? 1 : chunk_rows(D, sel != nullptr);
     s = cuda_status(launch_paged_tc(D, G, q, k_pages, v_pages, sel, out, from,
                                     scratch + round256(paged_rows_workspace(D)), status, st));
     if (s != QSA_OK || from == 1) return s;
     rows_below = from;
   }
-  return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, rows_below, scratch, status, st));
+  return cuda_status(launch_paged_rows(D, G, q, k_pages, v_pages, sel, out, rows_below, scratch, status, st, tc));
 }
 
 qsa_status_t qsa_read_device_status(void *workspace, qsa_stream_t stream, qsa_status_t *status) {

@@ -254,18 +254,19 @@ cudaError_t launch_paged_append(const Dims &D, const NormRope &N, const Paged &P
 
 // Attention over the paged cache, few (token, head) rows per sequence or shapes that the
 // tensor-core chunk kernels do not serve; sel null: every visible token. Sequences with
-// max_rows or more (token, head) rows are left out.
+// max_rows or more (token, head) rows are left out. pdl: as a programmatic dependent of
+// launch_paged_tc's kernels, with which it shares no data but inputs.
 size_t paged_rows_workspace(const Dims &D);
 cudaError_t launch_paged_rows(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
                               const int32_t *sel, void *out, long long max_rows, void *scratch, int *status,
-                              cudaStream_t st);
+                              cudaStream_t st, bool pdl);
 
 // The same for sequences of at least min_rows rows on tcgen05 tensor cores.
 bool paged_tc_supported(const Dims &D, const Paged &P, bool sel);
 size_t paged_tc_workspace(const Dims &D);
 cudaError_t launch_paged_tc(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st);
-// The one-tile form of launch_paged_tc (head_dim 128 and 256).
+// The one-tile form of launch_paged_tc (head_dim 64, 128 and 256).
 size_t paged_tc1_workspace(const Dims &D);
 cudaError_t launch_paged_tc1(const Dims &D, const Paged &P, const void *q, const void *k_pages, const void *v_pages,
                              const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st);

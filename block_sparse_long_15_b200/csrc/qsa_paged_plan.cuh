@@ -382,7 +382,8 @@ __device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea
 constexpr int kMergeWarps = 16, kMergeRows = kMergeWarps;
 template <class X>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {
-  pdl_wait();  // the parts come from the kernel before
+  pdl_trigger();  // the row kernel behind it, where there is one, needs nothing of this one
+  pdl_wait();     // the parts come from the kernel before
   const int c = blockIdx.x;
   const MergeJob J = P.jobs[c];
   if (J.c_last < 0) return;
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_c
   const int rr = blockIdx.y * kMergeRows + (threadIdx.x >> 5), row = rr % kRows;  // row of tile rr / 128
   const int tok = J.r0 + rr / kRows * P.T + row / P.D.G;
   if (row / P.D.G >= P.T || tok >= J.n) return;
+  const bool mine = X::kD >= 128 || col < X::kD;
   auto place = [&](int p) { return (size_t)(p == c ? J.s0 : 2 * p) * (X::kTiles * kRows) + rr; };
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_c
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         w[e] = __shfl_sync(0xffffffffu, f, (p1 + e) & 31);
-        const bool in = p1 + e < n && w[e] > 0.f;  // a part that sees nothing of the row left nothing
+        const bool in = mine && p1 + e < n && w[e] > 0.f;  // a part that sees nothing of the row left nothing
         if (!in) w[e] = 0.f;
         x[e] = in ? *(const float4 *)(P.part_o + place(p0 + p1 + e) * X::kD + col) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_c
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   __nv_bfloat16 *dst = P.out + (((size_t)J.q0 + tok) * P.D.Hq + J.g * P.D.G + row % P.D.G) * X::kD + col;
-  *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (mine) *(uint2 *)dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 // ---------------------------------------------------------------- host side
@@ -507,7 +509,7 @@ cudaError_t launch_chunks(Launch launch, size_t (*smem_of)(bool, int), const Dim
     cudaError_t e = launch(P, tk, tv, smem_of(sel != nullptr, P.nb));
     if (e == cudaSuccess) {
       note_launch();
-      e = launch_maybe_pdl(k_paged_merge<X>, dim3(P.C, X::kTiles * kRows / kMergeRows, X::kD / 128),
+      e = launch_maybe_pdl(k_paged_merge<X>, dim3(P.C, X::kTiles * kRows / kMergeRows, (X::kD + 127) / 128),
                            dim3(kMergeWarps * 32), 0, st, true, P);
     }
     if (e != cudaSuccess) {

@@ -757,15 +757,14 @@ int sm_count() {
 int ctas_per_sm(size_t smem) { return std::max(1, std::min(3, (int)(228 * 1024 / (smem + 1024)))); }
 
 template <int D, int NT>
-cudaError_t launch_mma(RowsParams &P, cudaStream_t st) {
+cudaError_t launch_mma(RowsParams &P, cudaStream_t st, bool pdl) {
   typedef MmaLayout<D, NT> Y;
   const size_t smem = Y::kOffPlan + plan_bytes(P.nb);
   P.C = min(sm_count() * ctas_per_sm(smem), kMaxCtas);
   cudaError_t e = ensure_smem(k_paged_rows<D, NT>, smem);
   if (e != cudaSuccess) return e;
   note_launch();
-  k_paged_rows<D, NT><<<P.C, kThreads, smem, st>>>(P);
-  return cudaGetLastError();
+  return launch_maybe_pdl(k_paged_rows<D, NT>, dim3(P.C), dim3(kThreads), smem, st, pdl, P);
 }
 
 template <typename T>
@@ -789,7 +788,7 @@ size_t paged_rows_workspace(const Dims &D) {
 
 cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
                               const int32_t *sel, void *out, long long max_rows, void *scratch, int *status,
-                              cudaStream_t st) {
+                              cudaStream_t st, bool pdl) {
   RowsParams P;
   P.Hq = D.Hq;
   P.Hkv = D.Hkv;
@@ -819,9 +818,9 @@ cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, cons
     P.nb = min(kMaxSeqs, G.batch - P.b0);
     cudaError_t e;
     if (!mma) e = D.bf16 ? launch_simt<__nv_bfloat16>(P, st) : launch_simt<float>(P, st);
-    else if (D.d == 64) e = P.R == 8 ? launch_mma<64, 1>(P, st) : launch_mma<64, 2>(P, st);
-    else if (D.d == 128) e = P.R == 8 ? launch_mma<128, 1>(P, st) : launch_mma<128, 2>(P, st);
-    else e = P.R == 8 ? launch_mma<256, 1>(P, st) : launch_mma<256, 2>(P, st);
+    else if (D.d == 64) e = P.R == 8 ? launch_mma<64, 1>(P, st, pdl) : launch_mma<64, 2>(P, st, pdl);
+    else if (D.d == 128) e = P.R == 8 ? launch_mma<128, 1>(P, st, pdl) : launch_mma<128, 2>(P, st, pdl);
+    else e = P.R == 8 ? launch_mma<256, 1>(P, st, pdl) : launch_mma<256, 2>(P, st, pdl);
     if (e != cudaSuccess) {
       note_error("paged attention launch", e);
       return e;

@@ -128,6 +128,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  pdl_trigger();  // the merge may take its place; it waits for this kernel's end
 
   if (warp == kBuilderWarp) {
     const SlotArea area = {&bars[kBarSlotFull], &bars[kBarSlotFree], base + kOffInfo, base + kOffBits, abort_flag};
@@ -555,19 +556,19 @@ static_assert(1024 + kOffBits + 2 * kBitSlotBytes + plan_bytes(kMaxSeqs) <= 227 
 
 }  // namespace
 
-// bf16, head_dim 128 or 256, blocks of whole 64-key halves.
+// bf16, head_dim 64, 128 or 256, blocks of whole 64-key halves.
 bool paged_tc_supported(const Dims &D, const Paged &G, bool sel) {
-  return D.bf16 && (D.d == 128 || D.d == 256) && D.G <= 32 && (!sel || D.B % kHalf == 0) &&
+  return D.bf16 && (D.d == 64 || D.d == 128 || D.d == 256) && D.G <= 32 && (!sel || D.B % kHalf == 0) &&
          (long long)G.n_pages * D.Hkv <= 0x7fffffffLL;
 }
 
 // The one-tile kernel takes less.
-size_t paged_tc_workspace(const Dims &D) { return D.d == 256 ? paged_tc1_workspace(D) : partials_bytes<Two128>(); }
+size_t paged_tc_workspace(const Dims &D) { return D.d != kD ? paged_tc1_workspace(D) : partials_bytes<Two128>(); }
 
 cudaError_t launch_paged_tc(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
   // Sequences whose rows fill no more than one tile leave the second one idle.
-  if (D.d == 256 || (long long)G.max_chunk * D.G <= kRows)
+  if (D.d != kD || (long long)G.max_chunk * D.G <= kRows)
     return launch_paged_tc1(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
   CUtensorMap tq;
   if (!encode_fn() || !make_map(&tq, q, kD, D.Hq, G.n_tok, D.G, kRows / D.G)) {

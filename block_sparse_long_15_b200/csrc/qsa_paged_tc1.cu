@@ -1,6 +1,6 @@
 // Attention of chunks of new tokens over a paged K/V cache on 5th-generation tensor cores
-// (tcgen05), one 128-row tile per CTA: head_dim 256, and head_dim 128 for sequences of no more
-// than 128 (token, head) rows. See qsa_paged_tc.cu for head_dim 128 otherwise and
+// (tcgen05), one 128-row tile per CTA: head_dim 256 and 64, and head_dim 128 for sequences of no
+// more than 128 (token, head) rows. See qsa_paged_tc.cu for head_dim 128 otherwise and
 // qsa_paged_plan.cuh for how the work is divided.
 //
 // At head_dim 256 O of one tile takes 256 TMEM columns, so a CTA holds T = 128 / G tokens of one
@@ -10,8 +10,8 @@
 // its 64 columns would need with both operands there, and shared memory is left to 192 KB of K and
 // V stages. S is double-buffered, so the softmax of a chunk runs beside the products of its
 // neighbours:
-//   warp 0      TMA producer: K and V of a chunk into two rings, 3 deep (6 at head_dim 128); one
-//               lane per page box and 64 columns;
+//   warp 0      TMA producer: K and V of a chunk into two rings, 3 deep (6 at head_dim 128, 8 at 64);
+//               one lane per page box and 64 columns;
 //   warp 1      MMA issuer (TMEM owner): O += P(n) V, S = Q K(n + 2)^T into the buffer that
 //               P(n) has just left;
 //   warp 2      builder;
@@ -38,7 +38,7 @@ constexpr uint32_t kGroupBytes = kChunk * 128;  // 64 columns of a chunk's rows
 
 template <int D_>
 struct Layout {
-  static constexpr int kNR = D_ == 256 ? 3 : 6;      // depth of each ring
+  static constexpr int kNR = D_ == 256 ? 3 : D_ == 128 ? 6 : 8;  // depth of each ring
   static constexpr int kGroups = D_ / 64;
   static constexpr uint32_t kStageBytes = kChunk * D_ * 2;
   static constexpr uint32_t kColQ = D_, kColS = D_ + D_ / 2;
@@ -110,6 +110,7 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  pdl_trigger();  // the merge may take its place; it waits for this kernel's end
 
   if (warp == kBuilderWarp) {
     const SlotArea area = {&bars[Y::kBarSlotFull], &bars[Y::kBarSlotFree], base + Y::kOffInfo, base + Y::kOffBits, abort_flag};
@@ -308,11 +309,11 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         m_ref = -INFINITY;
         l = 0.f;
         // Q of the unit, once every QK of the unit before has completed
-        constexpr int kQ = kD / 128;  // 64 dims at a time
+        constexpr int kQ = (kD + 127) / 128;  // 64 dims at a time (32 at head_dim 64)
         uint32_t q[kQ][32];
         const uint4 *src = (const uint4 *)(P.q + at);
 #pragma unroll
-        for (int i = 0; i < 8 * kQ; ++i) {
+        for (int i = 0; i < kD / 16; ++i) {
           const uint4 x = valid ? src[i] : make_uint4(0, 0, 0, 0);
           uint32_t *d = &q[i / 8][4 * (i % 8)];
           d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
@@ -323,7 +324,9 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < kQ; ++i) tmem_st32_split<kD / 4>(lane_addr + Y::kColQ + 32 * i, q[i]);
+        for (int i = 0; i < kQ; ++i)
+          if (kD == 64) tmem_st16_split_lo<16>(lane_addr + Y::kColQ, q[i]);
+          else tmem_st32_split<kD / 4>(lane_addr + Y::kColQ + 32 * i, q[i]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -483,13 +486,13 @@ cudaError_t launch_d(const Dims &D, const Paged &G, const void *q, const void *k
 }  // namespace
 
 size_t paged_tc1_workspace(const Dims &D) {
-  return D.d == 256 ? partials_bytes<One<256>>() : partials_bytes<One<128>>();
+  return D.d == 256 ? partials_bytes<One<256>>() : D.d == 128 ? partials_bytes<One<128>>() : partials_bytes<One<64>>();
 }
 
 cudaError_t launch_paged_tc1(const Dims &D, const Paged &G, const void *q, const void *k_pages, const void *v_pages,
                              const int32_t *sel, void *out, int min_rows, void *scratch, int *status, cudaStream_t st) {
-  return D.d == 256 ? launch_d<256>(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st)
-                    : launch_d<128>(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
+  auto launch = D.d == 256 ? launch_d<256> : D.d == 128 ? launch_d<128> : launch_d<64>;
+  return launch(D, G, q, k_pages, v_pages, sel, out, min_rows, scratch, status, st);
 }
 
 }  // namespace qsa

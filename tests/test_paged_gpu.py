@@ -170,6 +170,8 @@ CASES = [
     ("bf16", 24, 8, 128, 256, 64, 0, [42, 7], [3000, 2000]),
     ("bf16", 32, 1, 256, 32, 64, 0, [4, 1, 3], [5000, 1, 700]),
     ("bf16", 16, 2, 256, 16, 128, 3, [12, 8], [5000, 2300]),
+    ("bf16", 24, 8, 64, 32, 64, 0, [30, 2, 500], [3000, 900, 700]),
+    ("bf16", 8, 1, 64, 16, 64, 3, [3, 60], [900, 2500]),
     # many rows and many parts
     ("bf16", 16, 2, 128, 32, 64, 0, [300, 40], [4100, 40]),
     ("bf16", 16, 2, 128, 128, 192, 6, [300, 40], [4100, 2100]),
@@ -181,7 +183,7 @@ CASES = [
 ]
 
 
-def _run(qsa, case, seed=11, std=1.0, poison=NAN, lead=1, tail=2):
+def _run(qsa, case, seed=11, std=1.0, poison=NAN, lead=1, tail=2, pick=None):
     dtype, Hq, Hkv, d, page, block, topk, q_len, kv_len = case
     dt = DT[dtype]
     g = U.make_batch(q_len, kv_len, page, seed=seed, lead=lead, tail=tail)
@@ -194,7 +196,9 @@ def _run(qsa, case, seed=11, std=1.0, poison=NAN, lead=1, tail=2):
     sel = None
     if topk:
         sel = torch.full((g["n_tok"], topk), 12345, dtype=torch.int32)
-        sel[lead:g["n_tok"] - tail] = U.selection(q_len, kv_len, block, topk, seed + 3)
+        mine = sel[lead:g["n_tok"] - tail]
+        mine[:] = -1
+        mine[:, : pick or topk] = U.selection(q_len, kv_len, block, pick or topk, seed + 3)
         sel = sel.cuda()
     pg = qsa.make_paged(**g)
     out = torch.full_like(q, 7.0)
@@ -211,6 +215,37 @@ def _oracle(s, case):
     r = s["rows"]
     return U.attention(s["q"][r], s["kp"], s["vp"], s["g"]["page_table"], q_len, kv_len, 1 / math.sqrt(d), block,
                        None if s["sel"] is None else s["sel"][r])
+
+
+# A large budget sends chunks with a selection to the tensor-core kernels; `pick` entries of each list
+# are used, the rest is -1.
+TILE_CASES = [
+    # pick, case
+    (5, ("bf16", 16, 2, 128, 64, 64, 256, [100, 13, 3], [4100, 700, 300])),
+    (3, ("bf16", 16, 2, 128, 16, 192, 128, [16, 12, 15], [3000, 2999, 1024])),   # one tile
+    (7, ("bf16", 24, 8, 128, 128, 128, 128, [90, 0, 41, 2], [2000, 5, 1300, 200])),  # G = 3: idle rows
+    (1, ("bf16", 16, 2, 256, 32, 64, 256, [70, 12], [2500, 640])),
+    (4, ("bf16", 8, 1, 64, 256, 64, 512, [129, 60], [3300, 900])),
+    # lists longer than one segment's bits: every group of one head
+    (9, ("bf16", 2, 2, 128, 64, 64, 1024, [200], [16000])),
+    (9, ("bf16", 1, 1, 256, 64, 128, 1024, [40], [33000])),
+]
+
+
+@pytest.mark.parametrize("pick,case", TILE_CASES, ids=lambda c: str(c) if isinstance(c, int) else
+                         "-".join(str(x) for x in c[:7]) + f"-q{max(c[7])}-kv{max(c[8])}")
+def test_attention_selected_tiles(cuda_lib, pick, case):
+    qsa = cuda_lib
+    s = _run(qsa, case, pick=pick)
+    n0 = qsa.qsa_kernel_launch_count()
+    _attn(qsa, s)
+    assert qsa.qsa_kernel_launch_count() - n0 >= 2  # a tile kernel and the merge
+    assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK
+    U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+    assert (s["out"][:1] == 7).all() and (s["out"][-2:] == 7).all()
+    first = s["out"].clone()
+    _attn(qsa, s)
+    assert torch.equal(first, s["out"])
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c[:7]) + f"-q{max(c[7])}-kv{max(c[8])}")
