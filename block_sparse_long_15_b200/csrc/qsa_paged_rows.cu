@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qsa_internal.h"
 #include "sm100_ptx.cuh"
@@ -583,8 +584,11 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
 
 // ---------------------------------------------------------------- any type and shape, CUDA cores
 // fp32, and bf16 head widths or block sizes without a tensor-core form: the same items, two
-// tiles at a time for the whole CTA. Lanes are keys for the logits (4 rows a warp) and
-// dims for the output; everything in fp32.
+// tiles at a time for the whole CTA. Lanes are keys for the logits and dims for the output;
+// everything in fp32. Latency bounds it (a selection, a page table and the keys, one after the
+// other): the pool rows of up to 32 tiles are looked up at once, the rows are dealt out to the warps
+// one by one, and several CTAs share an SM.
+constexpr int kLookTiles = 32;
 constexpr int kSimtKeys = 2 * kTile;
 
 template <typename T>
@@ -598,15 +602,78 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
+// One step of a warp: its first N rows (qs, kWarps d apart) against the 32 keys in shared memory; lane
+// `key` is the key's position, beyond every row's where nobody sees it.
+constexpr int kRW = kMaxRows / kWarps;  // rows per warp
+template <int N, bool kHi>  // kHi: d > 128, a second group of dims
+__device__ __forceinline__ void simt_step(const float *ks, const float *vs, const float *qs, int d, int key,
+                                          const int (&trow)[kRW], float sl2, float (&m)[kRW], float (&l)[kRW],
+                                          float4 (&o)[kRW][2]) {
+  const int lane = threadIdx.x & 31;
+  float acc[N], p[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) acc[r] = 0.f;
+  const float *kr = ks + lane * (d + 4);
+#pragma unroll 4
+  for (int c4 = 0; c4 < d; c4 += 4) {
+    const float4 x = *(const float4 *)(kr + c4);
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float4 y = *(const float4 *)(qs + r * kWarps * d + c4);
+      acc[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[r]))));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const float x = key <= trow[r] ? acc[r] * sl2 : -INFINITY;
+    float mx = x;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float mn = fmaxf(m[r], mx);
+    const float f = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
+    p[r] = x == -INFINITY ? 0.f : ex2_approx(x - mn);
+    l[r] = fmaf(l[r], f, p[r]);
+    m[r] = mn;
+#pragma unroll
+    for (int q = 0; q < (kHi ? 2 : 1); ++q) {
+      o[r][q].x *= f;
+      o[r][q].y *= f;
+      o[r][q].z *= f;
+      o[r][q].w *= f;
+    }
+  }
+  const bool lo = lane * 4 < d, hi = 128 + lane * 4 < d;  // the lane's two groups of four dims
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 x = lo ? *(const float4 *)(vs + k * d + lane * 4) : zero;
+    const float4 y = kHi && hi ? *(const float4 *)(vs + k * d + 128 + lane * 4) : zero;
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float pk = __shfl_sync(0xffffffffu, p[r], k);
+      o[r][0].x = fmaf(pk, x.x, o[r][0].x);
+      o[r][0].y = fmaf(pk, x.y, o[r][0].y);
+      o[r][0].z = fmaf(pk, x.z, o[r][0].z);
+      o[r][0].w = fmaf(pk, x.w, o[r][0].w);
+      if (kHi) {
+        o[r][1].x = fmaf(pk, y.x, o[r][1].x);
+        o[r][1].y = fmaf(pk, y.y, o[r][1].y);
+        o[r][1].z = fmaf(pk, y.z, o[r][1].z);
+        o[r][1].w = fmaf(pk, y.w, o[r][1].w);
+      }
+    }
+  }
+}
+
 size_t simt_fixed_bytes(int d) {  // K, V, q, O of the CTA
   return sizeof(float) * ((size_t)kSimtKeys * (2 * d + 4) + 2 * (size_t)kMaxRows * (d + 1));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__ RowsParams P, int fixed) {
+__global__ void __launch_bounds__(kThreads, 4) k_paged_simt(const __grid_constant__ RowsParams P, int fixed) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_key0[2], s_nv[2];
-  __shared__ long long s_row[kSimtKeys];
+  __shared__ int s_key0[kLookTiles];
+  __shared__ long long s_row[kLookTiles * kTile];  // pool row of a key, -1: nobody sees it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = P.d, d4 = d >> 2;
   float *ks = (float *)smem;            // [32][d + 4]
@@ -619,7 +686,6 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__
   const int c = blockIdx.x;
   if (c >= L.C) return;
   const long long lo = div_pos((long long)c * L.T, L.C), hi = div_pos((long long)(c + 1) * L.T, L.C);
-  constexpr int kRW = kMaxRows / kWarps;  // rows per warp
 
   for (long long i0 = lo; i0 < hi;) {
     const Unit u = unit_of(P, L, i0);
@@ -631,35 +697,36 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__
       if (unit_row(P, u, r, tok, h)) x = load4((const T *)P.q + ((size_t)(u.s.q0 + tok) * P.Hq + u.g * P.G + h) * d + c4);
       *(float4 *)(qs + r * d + c4) = x;
     }
-    int trow[kRW];
+    int trow[kRW], n_mine = 0;  // row r of the warp is row kWarps r + warp of the unit; valid ones come first
     float m[kRW], l[kRW];
     float4 o[kRW][2];
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
       int tok, h;
-      const bool in = unit_row(P, u, warp * kRW + r, tok, h);
+      const bool in = unit_row(P, u, r * kWarps + warp, tok, h);
       trow[r] = in ? u.s.len - u.s.n + tok : -1;
+      if (in) n_mine = r + 1;
       m[r] = -INFINITY;
       l[r] = 0.f;
       o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const bool mine = trow[0] >= 0;  // rows are dealt out in order: without the first there is none
     for (long long i = i0; i < i1; i += 2) {
+      const int look = (int)(i - i0) % kLookTiles;
       __syncthreads();
-      if (threadIdx.x < kSimtKeys) {
-        const int half = threadIdx.x / kTile, kk = threadIdx.x % kTile;
-        int key0 = 0, nv = 0;
-        if (i + half < i1) tile_keys(P, u, (int)(i + half - u.first), key0, nv);
-        s_row[threadIdx.x] = kk < nv ? key_row(P, u, key0 + kk) : -1;
-        if (kk == 0) {
-          s_key0[half] = key0;
-          s_nv[half] = nv;
+      if (look == 0) {
+        const int n_look = (int)min((long long)kLookTiles, i1 - i);
+        for (int e = threadIdx.x; e < kLookTiles * kTile; e += kThreads) {
+          int key0 = 0, nv = 0;
+          if (e / kTile < n_look) tile_keys(P, u, (int)(i - u.first) + e / kTile, key0, nv);
+          s_row[e] = e % kTile < nv ? key_row(P, u, key0 + e % kTile) : -1;
+          if (e % kTile == 0) s_key0[e / kTile] = key0;
         }
+        __syncthreads();
       }
-      __syncthreads();
+      const long long *rows = s_row + look * kTile;
       for (int e = threadIdx.x; e < kSimtKeys * d4; e += kThreads) {
         const int kk = e / d4, c4 = (e - kk * d4) * 4;
-        const long long row = s_row[kk];
+        const long long row = rows[kk];
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (row >= 0) {
           x = load4((const T *)P.kp + (size_t)row * d + c4);
@@ -669,63 +736,23 @@ __global__ void __launch_bounds__(kThreads) k_paged_simt(const __grid_constant__
         *(float4 *)(vs + kk * d + c4) = y;
       }
       __syncthreads();
-      if (!mine) continue;
-      float acc[kRW];
-#pragma unroll
-      for (int r = 0; r < kRW; ++r) acc[r] = 0.f;
-      for (int c4 = 0; c4 < d; c4 += 4) {
-        const float4 x = *(const float4 *)(ks + lane * (d + 4) + c4);
-#pragma unroll
-        for (int r = 0; r < kRW; ++r) {
-          const float4 y = *(const float4 *)(qs + (warp * kRW + r) * d + c4);
-          acc[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[r]))));
-        }
-      }
-      const int key = s_key0[lane / kTile] + lane % kTile;
-      const bool in = s_row[lane] >= 0;
-      float p[kRW];
-#pragma unroll
-      for (int r = 0; r < kRW; ++r) {
-        const float x = in && key <= trow[r] ? acc[r] * P.sl2 : -INFINITY;
-        float mx = x;
-#pragma unroll
-        for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        const float mn = fmaxf(m[r], mx);
-        const float f = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
-        p[r] = x == -INFINITY ? 0.f : ex2_approx(x - mn);
-        l[r] = fmaf(l[r], f, p[r]);
-        m[r] = mn;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          o[r][q].x *= f;
-          o[r][q].y *= f;
-          o[r][q].z *= f;
-          o[r][q].w *= f;
-        }
-      }
-#pragma unroll 4
-      for (int k = 0; k < kSimtKeys; ++k) {
-        float pk[kRW];
-#pragma unroll
-        for (int r = 0; r < kRW; ++r) pk[r] = __shfl_sync(0xffffffffu, p[r], k);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int c4 = q * 128 + lane * 4;
-          if (c4 >= d) continue;
-          const float4 x = *(const float4 *)(vs + k * d + c4);
-#pragma unroll
-          for (int r = 0; r < kRW; ++r) {
-            o[r][q].x = fmaf(pk[r], x.x, o[r][q].x);
-            o[r][q].y = fmaf(pk[r], x.y, o[r][q].y);
-            o[r][q].z = fmaf(pk[r], x.z, o[r][q].z);
-            o[r][q].w = fmaf(pk[r], x.w, o[r][q].w);
-          }
-        }
-      }
+      if (n_mine == 0) continue;
+      const int key = rows[lane] >= 0 ? s_key0[look + lane / kTile] + lane % kTile : 0x7fffffff;
+      auto step = [&](auto n, auto hi) {
+        simt_step<decltype(n)::value, decltype(hi)::value>(ks, vs, qs + warp * d, d, key, trow, P.sl2, m, l, o);
+      };
+      auto pick = [&](auto hi) {
+        if (n_mine == 1) step(std::integral_constant<int, 1>{}, hi);
+        else if (n_mine == 2) step(std::integral_constant<int, 2>{}, hi);
+        else if (n_mine == 3) step(std::integral_constant<int, 3>{}, hi);
+        else step(std::integral_constant<int, 4>{}, hi);
+      };
+      if (d > 128) pick(std::true_type{});
+      else pick(std::false_type{});
     }
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
-      const int row = warp * kRW + r;
+      const int row = r * kWarps + warp;
 #pragma unroll
       for (int s = 16; s; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
       if (lane == 0) {
@@ -753,14 +780,14 @@ int sm_count() {
   return n[dev];
 }
 
-// CTAs whose shared memory an SM holds at once (228 KB, 1 KB of it reserved per CTA), 3 at most
-int ctas_per_sm(size_t smem) { return std::max(1, std::min(3, (int)(228 * 1024 / (smem + 1024)))); }
+// CTAs whose shared memory an SM holds at once (228 KB, 1 KB of it reserved per CTA), `most` at most
+int ctas_per_sm(size_t smem, int most) { return std::max(1, std::min(most, (int)(228 * 1024 / (smem + 1024)))); }
 
 template <int D, int NT>
 cudaError_t launch_mma(RowsParams &P, cudaStream_t st, bool pdl) {
   typedef MmaLayout<D, NT> Y;
   const size_t smem = Y::kOffPlan + plan_bytes(P.nb);
-  P.C = min(sm_count() * ctas_per_sm(smem), kMaxCtas);
+  P.C = min(sm_count() * ctas_per_sm(smem, 3), kMaxCtas);
   cudaError_t e = ensure_smem(k_paged_rows<D, NT>, smem);
   if (e != cudaSuccess) return e;
   note_launch();
@@ -771,7 +798,7 @@ template <typename T>
 cudaError_t launch_simt(RowsParams &P, cudaStream_t st) {
   const size_t fixed = (simt_fixed_bytes(P.d) + 15) & ~(size_t)15;
   const size_t smem = fixed + plan_bytes(P.nb);
-  P.C = min(sm_count() * ctas_per_sm(smem), kMaxCtas);
+  P.C = min(sm_count() * ctas_per_sm(smem + 4608, 4), kMaxCtas);
   cudaError_t e = ensure_smem(k_paged_simt<T>, smem);
   if (e != cudaSuccess) return e;
   note_launch();
