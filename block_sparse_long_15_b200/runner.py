@@ -140,3 +140,105 @@ class QSADecodeOffload(QSADecode):
     def __call__(self, stream=None):
         qsa.qsa_decode_offload(self.cfg, self.t, self.staging, self.ws, stream)
         return self.t["out"], self.t["sel"]
+
+
+class QSAPaged:
+    """A paged K/V cache and the steps that serve from it: chunks of prompts, drafted tokens, decode.
+
+    Owns the pools [n_pages][Hkv][page_size][d], the page table and the indexer state (one plane per
+    slot) of a fixed number of sequence slots, and the free pages. A step takes the packed rows of every
+    slot's new tokens (a slot may have none), appends them with norm and rotation on the way and
+    attends: over everything, or, given indexer rows, over the blocks that the indexer selects. Page
+    numbers are handed out on the host; all arithmetic runs in libqsa.so.
+    """
+
+    def __init__(self, cfg, slots: int, max_len: int, n_pages: int, page_size: int, norm_rope=None, device="cuda"):
+        B, di = cfg.indexer_compress_ratio, cfg.indexer_head_dim
+        dt = torch.bfloat16 if cfg.dtype == qsa.QSA_DTYPE_BF16 else torch.float32
+        self.cfg, self.nr, self.device, self.dtype = cfg, norm_rope, device, dt
+        self.slots, self.max_len, self.page_size, self.n_pages = slots, max_len, page_size, n_pages
+        pool = (n_pages, cfg.num_key_value_heads, page_size, cfg.head_dim)
+        self.k_pages = torch.zeros(pool, dtype=dt, device=device)
+        self.v_pages = torch.zeros(pool, dtype=dt, device=device)
+        self.ki_cache = torch.zeros(slots, max_len, di, dtype=dt, device=device)
+        self.kbar_cache = torch.zeros(slots, max_len // B, di, dtype=torch.float32, device=device)
+        self.kbar_blocks = torch.zeros(slots, dtype=torch.int32, device=device)
+        self.kv_start = torch.zeros(slots, dtype=torch.int32, device=device)
+        self.table = torch.zeros(slots, -(-max_len // page_size), dtype=torch.int32)
+        self.length = [0] * slots
+        self.pages = [[] for _ in range(slots)]
+        self.free = list(range(n_pages - 1, -1, -1))
+        self.ws = self.score_ws = None
+
+    def release(self, slot: int):
+        """The slot's sequence has ended: its pages go back."""
+        self.free += reversed(self.pages[slot])
+        self.pages[slot], self.length[slot] = [], 0
+        self.kbar_blocks[slot] = 0
+
+    def reserve(self, counts):
+        """Room for counts[s] more tokens of every slot s: for all of them or, with an error, for none."""
+        if len(counts) != self.slots:
+            raise ValueError(f"{len(counts)} counts for {self.slots} slots")
+        need = []
+        for s, n in enumerate(counts):
+            if n < 0 or self.length[s] + n > self.max_len:
+                raise ValueError(f"slot {s}: {self.length[s]} + {n} tokens, room for {self.max_len}")
+            need.append(-(-(self.length[s] + n) // self.page_size) - len(self.pages[s]))
+        if sum(need) > len(self.free):
+            raise ValueError(f"{sum(need)} pages needed, {len(self.free)} free")
+        for s, (n, m) in enumerate(zip(counts, need)):
+            for _ in range(m):
+                self.table[s, len(self.pages[s])] = self.free[-1]
+                self.pages[s].append(self.free.pop())
+            self.length[s] += n
+
+    def batch(self, counts):
+        """The packed batch of counts[s] new tokens of every slot, whose lengths count them already."""
+        start = torch.tensor([0] + list(counts)).cumsum(0).to(torch.int32)
+        lens = torch.tensor(self.length, dtype=torch.int32)
+        return qsa.make_paged(start.to(self.device), lens.to(self.device), self.table.to(self.device),
+                              n_tok=sum(counts), max_chunk=max(counts), page_size=self.page_size, n_pages=self.n_pages)
+
+    def select(self, counts, qi, pg):
+        """Selection [n_tok][k] of the packed rows qi [n_tok][Hi][di]: compresses the blocks that the step
+        completed, then scores and selects with every slot's rows padded to the longest chunk."""
+        cfg, most = self.cfg, max(counts)
+        qsa.qsa_compress_blocks(cfg, self.ki_cache, self.kv_start, pg.kv_len, self.kbar_cache,
+                                blocks_done=self.kbar_blocks.clone(), kbar_blocks=self.kbar_blocks)
+        count = torch.tensor(counts)
+        seq = torch.repeat_interleave(torch.arange(self.slots), count).to(self.device)
+        row = torch.cat([torch.arange(c) for c in counts]).to(self.device)
+        padded = torch.zeros(self.slots, most, *qi.shape[1:], dtype=self.dtype, device=self.device)
+        padded[seq, row] = qi
+        sel = torch.empty(self.slots, most, qsa.qsa_topk_blocks(cfg), dtype=torch.int32, device=self.device)
+        need = qsa.qsa_workspace_size(cfg, qsa.QSA_PREFILL, self.slots, most, self.max_len)
+        if self.score_ws is None or self.score_ws.numel() < need:
+            self.score_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        q_first = pg.kv_len - count.to(torch.int32).to(self.device)
+        qsa.qsa_index_score_topk(cfg, padded, self.kbar_cache, pg.kv_len, q_first, self.max_len, sel, self.score_ws)
+        return sel[seq, row].contiguous()
+
+    def step(self, counts, q, k, v, qi=None, ki=None):
+        """counts[s] new tokens of every slot s, packed in that order: q [n_tok][Hq][d] and k, v
+        [n_tok][Hkv][d] before norm and rotation. With the indexer's qi [n_tok][Hi][di] (rotated) and ki
+        [n_tok][di] the step attends the selected blocks. Returns [n_tok][Hq][d]."""
+        if (qi is None) != (ki is None):
+            raise ValueError("qi and ki come together")
+        self.reserve(counts)
+        if sum(counts) == 0:
+            return torch.empty_like(q)
+        pg = self.batch(counts)
+        need = qsa.qsa_paged_workspace_size(self.cfg, pg)
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        turned, out = torch.empty_like(q), torch.empty_like(q)
+        qsa.qsa_paged_append(self.cfg, self.nr, pg, k, v, self.k_pages, self.v_pages, self.ws, q=q, q_out=turned, ki=ki,
+                             ki_cache=self.ki_cache if ki is not None else None)
+        sel = self.select(counts, qi, pg) if ki is not None else None
+        qsa.qsa_paged_attn(self.cfg, pg, turned, self.k_pages, self.v_pages, sel, out, self.ws)
+        return out
+
+    def status(self) -> int:
+        """First device status of the steps since the last reading (QSA_OK before the first step)."""
+        return qsa.QSA_OK if self.ws is None else qsa.qsa_read_device_status(self.ws)

@@ -325,9 +325,9 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
  * Serving from a paged cache. A serving process holds the K/V cache in pages that
  * its sequences share out among themselves, and runs a batch of sequences with a
  * few new tokens each: one for a decode step, some for drafted tokens, many for a
- * chunk of a prompt. A step is qsa_project (rotary_dim 0 leaves q and k unrotated),
- * qsa_paged_append, then, on a layer with QSA, qsa_compress_blocks and
- * qsa_index_score_topk on the indexer's own cache (which stays one plane per
+ * chunk of a prompt. A step is qsa_project (with q_first all zero, where its rotation
+ * is the identity), qsa_paged_append, then, on a layer with QSA, qsa_compress_blocks
+ * and qsa_index_score_topk on the indexer's own cache (which stays one plane per
  * sequence), and qsa_paged_attn over the pages. (The model page has paged caches
  * nowhere; the layouts here are this library's.)
  *
@@ -348,7 +348,8 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
  * new tokens than max_chunk or kv_len, kv_len beyond max_pages * page_size) or that
  * needs a page outside [0, n_pages) records QSA_ERR_DEVICE_CHECK in the workspace
  * status word; nothing out of range is read or written for it, its own rows and
- * slots are unspecified, and the other sequences are served. */
+ * slots are unspecified, and the other sequences are served (where q_start falls, the
+ * append may leave rows of others out too). */
 typedef struct {
   int32_t batch;             /* sequences */
   int32_t n_tok;             /* rows of the packed tensors */

@@ -155,3 +155,25 @@ def test_binding_checks_shapes(qsa):
                        torch.zeros(2, 4, dtype=torch.int32), n_tok=1, max_chunk=1, page_size=16, n_pages=4)
     with pytest.raises(ValueError):
         qsa._rows(torch.zeros(4, 2, 256)[:, :, ::2], torch.float32, (4, 2, 128), "q")
+
+
+def test_page_bookkeeping(qsa):
+    """Pages are handed out and taken back on the host; a step that does not fit changes nothing."""
+    from block_sparse_long_15_b200.runner import QSAPaged
+    r = QSAPaged(_cfg(qsa), slots=3, max_len=256, n_pages=6, page_size=64, device="cpu")
+    r.reserve([65, 0, 1])
+    assert [len(p) for p in r.pages] == [2, 0, 1] and r.length == [65, 0, 1] and len(r.free) == 3
+    r.reserve([63, 64, 0])
+    assert [len(p) for p in r.pages] == [2, 1, 1]
+    for s in range(3):
+        assert r.table[s, : len(r.pages[s])].tolist() == r.pages[s]
+    before = ([list(p) for p in r.pages], list(r.length), list(r.free))
+    for bad in ([1, 64, 64], [200, 0, 0], [0, -1, 0], [1, 1]):
+        with pytest.raises(ValueError):
+            r.reserve(bad)
+        assert ([list(p) for p in r.pages], list(r.length), list(r.free)) == before
+    r.release(0)
+    assert r.length[0] == 0 and len(r.free) == 4
+    assert sorted(r.free + sum(r.pages, [])) == list(range(6))
+    with pytest.raises(ValueError):
+        r.step([0, 0, 1], None, None, None, qi=None, ki=1)

@@ -261,3 +261,279 @@ def test_attention(cuda_lib, case):
     _attn(qsa, s)  # the workspace is as it was: the same bits again
     assert torch.equal(first, s["out"])
     assert int(s["ws"][:256].sum()) == 0
+
+
+# ------------------------------------------------------------------ lists, masks and values
+def test_attention_of_rows_that_see_nothing(cuda_lib):
+    """A selection that lists nothing at a block boundary leaves a row empty: it is written as zeros, and
+    the rows beside it are right. Both kernels."""
+    qsa = cuda_lib
+    for topk, q_len, kv_len in ((4, [3, 1], [64, 128]), (2048, [70, 64], [128, 64])):
+        case = ("bf16", 16, 2, 128, 16, 64, topk, q_len, kv_len)
+        s = _run(qsa, case, pick=1)
+        rows = s["sel"][s["rows"]]
+        rows[:] = -1  # row at position 63 (127): no block, no trailing token
+        _attn(qsa, s)
+        assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK
+        U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+        last = s["rows"].start + q_len[0] - 1
+        assert (s["out"][last] == 0).all()
+
+
+def test_ids_outside_the_candidates_are_skipped(cuda_lib):
+    qsa = cuda_lib
+    for topk, q_len, kv_len in ((4, [2], [700]), (2048, [70], [700])):
+        case = ("bf16", 16, 2, 128, 64, 64, topk, q_len, kv_len)
+        s = _run(qsa, case, pick=2)
+        s["sel"][s["rows"], 2] = 11      # n_c is 10: not a complete block before any of the rows
+        s["sel"][s["rows"], 3] = 2 ** 30
+        _attn(qsa, s)
+        U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+
+
+@pytest.mark.parametrize("q_len,kv_len,d", [([2], [300], 128), ([100], [400], 128), ([40], [400], 256), ([30], [90], 64)])
+def test_attention_extreme_logits(cuda_lib, q_len, kv_len, d):
+    """Logits of several thousand either way: one key takes (nearly) everything, the sums stay finite. The
+    bf16 inputs are exact in the oracle; the logits' own rounding, 2 d 2^-24 M, is in the tolerance."""
+    qsa = cuda_lib
+    case = ("bf16", 16, 2, d, 64, 64, 0, q_len, kv_len)
+    s = _run(qsa, case, std=4.0)
+    s["q"][s["rows"]] *= 16
+    _attn(qsa, s)
+    U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+
+
+def test_masked_infinities_in_keys(cuda_lib):
+    """Keys of later tokens of the chunk may be infinite: the mask is a selection, not a product."""
+    qsa = cuda_lib
+    for q_len, d in (([4], 128), ([100], 128), ([60], 256)):
+        case = ("bf16", 16, 2, d, 16, 64, 0, q_len, [q_len[0] + 37])
+        s = _run(qsa, case)
+        n = case[8][0] - 1
+        s["kp"][s["g"]["page_table"][0, n // 16].long(), :, n % 16] = float("inf")
+        _attn(qsa, s)
+        want, tol = _oracle(s, case)
+        got = s["out"][s["rows"]]
+        U.check(got[:-1], want[:-1], tol[:-1], "out")  # all but the token itself
+
+
+# ------------------------------------------------------------------ geometry that does not fit
+BAD = [("q_start falls", lambda g: g["q_start"].__setitem__(2, 0)),
+       ("q_start passes n_tok", lambda g: g["q_start"].__setitem__(3, 10 ** 6)),
+       ("kv_len below the chunk", lambda g: g["kv_len"].__setitem__(1, 3)),
+       ("kv_len beyond the table", lambda g: g["kv_len"].__setitem__(1, 2 ** 31 - 1)),
+       ("negative kv_len", lambda g: g["kv_len"].__setitem__(1, -5)),
+       ("a page outside the pool", lambda g: g["page_table"].__setitem__((1, 3), 10 ** 6)),
+       ("a negative page", lambda g: g["page_table"].__setitem__((1, 2), -1)),
+       ("more tokens than max_chunk", lambda g: g.__setitem__("max_chunk", 60))]
+
+
+@pytest.mark.parametrize("name,spoil", BAD, ids=[b[0] for b in BAD])
+@pytest.mark.parametrize("topk,d,dtype", [(0, 128, "bf16"), (0, 256, "bf16"), (2048, 128, "bf16"), (4, 128, "bf16"),
+                                          (4, 64, "fp32")])
+def test_bad_geometry_is_reported_and_kept_apart(cuda_lib, name, spoil, topk, d, dtype):
+    """Sequence 1 is spoilt; 0 and 2 are served (unless their own rows are in dispute) and nothing faults."""
+    qsa = cuda_lib
+    q_len, kv_len = [50, 64, 40], [300, 200, 90]
+    case = (dtype, 16, 2, d, 64, 64, topk, q_len, kv_len)
+    s = _run(qsa, case, pick=2 if topk else None)
+    want, tol = _oracle(s, case)
+    g = {k: v.clone() if torch.is_tensor(v) else v for k, v in s["g"].items()}
+    spoil(g)
+    pg = qsa.make_paged(**g)
+    s["ws"] = qsa.alloc_paged_workspace(s["cfg"], pg)
+    qsa.qsa_paged_attn(s["cfg"], pg, s["q"], s["kp"], s["vp"], s["sel"], s["out"], s["ws"])
+    assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_ERR_DEVICE_CHECK
+    r = s["rows"].start
+    if name != "q_start falls":
+        U.check(s["out"][r:r + 50], want[:50], tol[:50], "sequence 0")
+    if not name.startswith("q_start"):
+        U.check(s["out"][r + 114:r + 154], want[114:], tol[114:], "sequence 2")
+    # the append: the same report, and only slots of the sequence itself may move
+    dt = DT[dtype]
+    k = torch.randn(g["n_tok"], 2, d, device="cuda").to(dt)
+    kp, ws = s["kp"].clone(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qsa.qsa_paged_append(s["cfg"], None, pg, k, k, kp, s["vp"].clone(), ws)
+    assert qsa.qsa_read_device_status(ws) == qsa.QSA_ERR_DEVICE_CHECK
+    held = torch.zeros(g["n_pages"], dtype=torch.bool)
+    for b, n in enumerate(kv_len):
+        held[s["g"]["page_table"][b, : -(-n // 64)].cpu().long()] = True
+    free = (~held).nonzero()[:, 0].cuda()
+    assert torch.equal(kp[free].view(torch.uint8), s["kp"][free].view(torch.uint8))
+
+
+def test_append_beyond_the_indexer_cache_is_reported(cuda_lib):
+    qsa = cuda_lib
+    g = U.make_batch([2, 2], [20, 9], 16, seed=5)
+    k = torch.randn(4, 2, 128).to(torch.bfloat16).cuda()
+    kp, vp = (torch.zeros(g["n_pages"], 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ki, ki_cache = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 19, 64, dtype=torch.bfloat16,
+                                                                                     device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qsa.qsa_paged_append(_cfg(qsa), None, qsa.make_paged(**g), k, k, kp, vp, ws, ki=ki, ki_cache=ki_cache)
+    assert qsa.qsa_read_device_status(ws) == qsa.QSA_ERR_DEVICE_CHECK
+    assert (ki_cache[0] == 0).all()  # the sequence that does not fit has no indexer key written
+    assert (ki_cache[1, 7:9] == 1).all() and (ki_cache[1, :7] == 0).all() and (ki_cache[1, 9:] == 0).all()
+
+
+# ------------------------------------------------------------------ streams, graphs, workspaces
+@pytest.mark.parametrize("case", [CASES[0], CASES[3], CASES[13], CASES[15], CASES[-1]], ids=["rows", "selected", "two-tile",
+                                                                                         "one-tile", "fp32"])
+def test_graphs_and_streams(cuda_lib, case):
+    """A captured call replays on new contents of the same tensors; two graphs and an eager call share one
+    workspace one after the other; a side stream gives the same bits."""
+    qsa = cuda_lib
+    s = _run(qsa, case, lead=0, tail=0, poison=0.0)
+    t = _run(qsa, case, seed=29, lead=0, tail=0, poison=0.0)
+    _attn(qsa, s)
+    want_s = s["out"].clone()
+    t["ws"] = s["ws"]
+    _attn(qsa, t)
+    want_t = t["out"].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s["out"].fill_(0)
+    side.wait_stream(torch.cuda.current_stream())
+    _attn(qsa, s, stream=side)
+    side.synchronize()
+    assert torch.equal(s["out"], want_s)
+    graphs = []
+    for x in (s, t):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _attn(qsa, x)
+        graphs.append(g)
+    for x in (s, t):
+        x["out"].fill_(0)
+    graphs[0].replay()
+    graphs[1].replay()
+    _attn(qsa, s)
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s["out"], want_s) and torch.equal(t["out"], want_t)
+    s["q"].copy_(t["q"])
+    s["kp"].copy_(t["kp"]) if s["kp"].shape == t["kp"].shape else None
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    again = s["out"].clone()
+    _attn(qsa, s)
+    assert torch.equal(again, s["out"])
+    assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK
+
+
+def test_append_and_norm_in_a_graph(cuda_lib):
+    qsa = cuda_lib
+    g = U.make_batch([1, 3], [20, 17], 16, seed=1)
+    q, k, v = (torch.randn(4, h, 128).to(torch.bfloat16).cuda() for h in (16, 2, 2))
+    kp, vp = (torch.zeros(g["n_pages"], 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    nr = qsa.make_norm_rope(w, w, rope_theta=1e6, rotary_dim=128)
+    pg, ws = qsa.make_paged(**g), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qo, pos = torch.empty_like(q), torch.arange(4, dtype=torch.int32, device="cuda")
+    qsa.qsa_paged_append(_cfg(qsa), nr, pg, k, v, kp, vp, ws, q=q, q_out=qo)  # modules are loaded before the capture
+    qsa.qsa_norm_rope(_cfg(qsa), nr, pos, q, None, q.clone(), None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qsa.qsa_paged_append(_cfg(qsa), nr, pg, k, v, kp, vp, ws, q=q, q_out=qo)
+    k.mul_(-1)
+    pg.kv_len.add_(1)
+    kp.zero_()
+    graph.replay()
+    want = torch.zeros_like(kp)
+    qsa.qsa_paged_append(_cfg(qsa), nr, pg, k, v, want, vp.clone(), ws)
+    assert torch.equal(kp, want) and int((kp != 0).any(-1).sum()) == 8
+
+
+def test_many_sequences(cuda_lib):
+    """More sequences than one launch of the attention takes, most of them with one token."""
+    qsa = cuda_lib
+    gen = torch.Generator().manual_seed(4)
+    q_len = torch.randint(0, 3, (1100,), generator=gen).tolist()
+    q_len[600] = 30
+    kv_len = [n + int(x) for n, x in zip(q_len, torch.randint(1, 60, (1100,), generator=gen))]
+    for d in (128, 256):
+        case = ("bf16", 8, 2, d, 16, 64, 0, q_len, kv_len)
+        s = _run(qsa, case)
+        _attn(qsa, s)
+        assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK
+        U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    k = torch.randn(s["g"]["n_tok"], 2, 256, device="cuda").to(torch.bfloat16)
+    qsa.qsa_paged_append(s["cfg"], None, s["pg"], k, k, s["kp"], s["vp"], ws)
+    assert qsa.qsa_read_device_status(ws) == qsa.QSA_OK
+    for r, b, t in U.positions(q_len, kv_len)[::97]:
+        assert torch.equal(s["kp"][int(s["g"]["page_table"][b, t // 16]), :, t % 16], k[r + 1])
+
+
+def test_shared_prefix_pages(cuda_lib):
+    """Two sequences over the same pages of a common prefix."""
+    qsa = cuda_lib
+    case = ("bf16", 16, 2, 128, 64, 64, 0, [1, 40], [128 + 5, 128 + 40])
+    s = _run(qsa, case)
+    s["g"]["page_table"][1, :2] = s["g"]["page_table"][0, :2]
+    _attn(qsa, s)
+    U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+
+
+# ------------------------------------------------------------------ a run of them together
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,block,topk,page", [("bf16", 16, 2, 128, 64, 3, 16), ("bf16", 16, 2, 256, 64, 3, 64),
+                                                          ("fp32", 4, 1, 64, 32, 4, 32)])
+@pytest.mark.parametrize("selected", [False, True])
+def test_serving_run(cuda_lib, dtype, Hq, Hkv, d, block, topk, page, selected):
+    """Prompts in chunks, then drafted tokens and single ones, slots coming and going: every output
+    against the plain form over what the cache should hold by then, every selection against
+    qsa_forward's on contiguous caches."""
+    from block_sparse_long_15_b200.runner import QSAPaged
+    qsa, dt, di, Hi = cuda_lib, DT[dtype], 64, 4
+    cfg = qsa.make_config(Hq, Hkv, d, Hi, di, block, topk, dtype)
+    gen = torch.Generator().manual_seed(12)
+    w = [(torch.randn(d, generator=gen) * 0.2 + 1).to(dt).cuda() for _ in range(2)]
+    rot, theta = d // 2, 1e6
+    nr = qsa.make_norm_rope(*w, eps=1e-6, rope_theta=theta, rotary_dim=rot, indexer_rotary_dim=64)
+    run = QSAPaged(cfg, slots=3, max_len=640, n_pages=3 * 640 // page, page_size=page, norm_rope=nr)
+    seen = [dict(k=[], v=[], ki=[]) for _ in range(3)]
+    steps = [[200, 0, 33], [130, 64, 1], [1, 1, 1], [4, 0, 3], "release 0", [70, 1, 0], [1, 1, 1]]
+    for counts in steps:
+        if counts == "release 0":
+            run.release(0)
+            seen[0] = dict(k=[], v=[], ki=[])
+            continue
+        n = sum(counts)
+        q, k, v = (torch.randn(n, h, d, generator=gen).to(dt).cuda() for h in (Hq, Hkv, Hkv))
+        qi, ki = (torch.randn(n, Hi, di, generator=gen).to(dt).cuda(), torch.randn(n, di, generator=gen).to(dt).cuda())
+        out = run.step(counts, q, k, v, qi if selected else None, ki if selected else None)
+        assert run.status() == qsa.QSA_OK
+        row = 0
+        for s, c in enumerate(counts):
+            mine = slice(row, row + c)
+            row += c
+            if c == 0:
+                continue
+            t0 = sum(len(x) for x in seen[s]["k"])
+            pos = torch.arange(t0, t0 + c, device="cuda")
+            # the library's own norm and rotation (tested above): the attention is in question here
+            qr, kr, pos32 = torch.empty_like(q[mine]), torch.empty_like(k[mine]), pos.to(torch.int32)
+            qsa.qsa_norm_rope(cfg, nr, pos32, q[mine], k[mine], qr, kr)
+            kir = U.rotate(ki[mine].double()[:, None], pos, 64, theta)[:, 0].to(dt)
+            for name, x in (("k", kr), ("v", v[mine]), ("ki", kir)):
+                seen[s][name].append(x)
+            length = t0 + c
+            K, V = (torch.cat(seen[s][x]).transpose(0, 1)[None] for x in ("k", "v"))  # one page of all tokens
+            sel = None
+            if selected:
+                assert run.length[s] == length
+                # the indexer keys that were stored are the rotated ones
+                U.check(run.ki_cache[s, :length], torch.cat(seen[s]["ki"]).double(),
+                        torch.full((length, di), U.HALF[dt] * 8, device="cuda"), "ki")
+                kbar = torch.zeros(1, 640 // block, di, device="cuda")
+                lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+                zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+                qsa.qsa_compress_blocks(cfg, run.ki_cache[s:s + 1], zero, lens, kbar)
+                sel = torch.empty(1, c, topk, dtype=torch.int32, device="cuda")
+                ws = qsa.alloc_workspace(cfg, qsa.QSA_PREFILL, 1, c, 640)
+                qsa.qsa_index_score_topk(cfg, qi[mine][None].contiguous(), kbar, lens, lens - c, 640, sel, ws)
+                sel = sel[0]
+            want, tol = U.attention(qr, K, V, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), [c], [length],
+                                    1 / math.sqrt(d), block, sel)
+            U.check(out[mine], want, tol, f"slot {s} after {t0} tokens")
+    assert sorted(run.free + sum(run.pages, [])) == list(range(run.n_pages))
