@@ -233,13 +233,13 @@ __device__ __forceinline__ bool idle_wait_warp(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// P for 32 keys held in registers (fp32 bits), written back in place over sv[0 .. 15] as bf16
-// pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds them to acc (the
-// fp32 values: only the product with V sees them in bf16).
-template <bool kAll>
+// P for keys kFrom .. kTo - 1 of 32 held in registers (fp32 bits), written back in place over
+// sv[kFrom / 2 ..] as bf16 pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds
+// them to acc (the fp32 values: only the product with V sees them in bf16).
+template <bool kAll, int kFrom = 0, int kTo = 32>
 __device__ __forceinline__ void p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2, uint64_t (&acc)[2]) {
 #pragma unroll
-  for (int u = 0; u < 32; u += 2) {
+  for (int u = kFrom; u < kTo; u += 2) {
     float p0, p1;
     f2_unpack(f2_fma(f2_pack(sv[u], sv[u + 1]), scale2, negm2), p0, p1);
     p0 = ex2_approx(p0);

@@ -54,8 +54,8 @@ struct Layout {
   static constexpr int kBarVFull = kBarKEmpty + kNR;
   static constexpr int kBarVEmpty = kBarVFull + kNR;
   static constexpr int kBarSFull = kBarVEmpty + kNR;     // [S buffer]
-  static constexpr int kBarPFull = kBarSFull + 2;        // [S buffer], 8 arrivals
-  static constexpr int kBarPVDone = kBarPFull + 2;       // a phase per PV
+  static constexpr int kBarPFull = kBarSFull + 2;        // [S buffer][step], 8 arrivals
+  static constexpr int kBarPVDone = kBarPFull + 4;       // a phase per PV
   static constexpr int kBarODone = kBarPVDone + 1;       // a phase per unit: its last PV completed
   static constexpr int kBarQFull = kBarODone + 1;        // a phase per unit: Q is in TMEM, 8 arrivals
   static constexpr int kBarQEmpty = kBarQFull + 1;       // a phase per unit: its last QK completed
@@ -89,7 +89,7 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < Y::kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == Y::kBarPFull || i == Y::kBarPFull + 1 || i == Y::kBarQFull) count = kSoftWarps;
+      if ((i >= Y::kBarPFull && i < Y::kBarPFull + 4) || i == Y::kBarQFull) count = kSoftWarps;
       if (i == Y::kBarSlotFull || i == Y::kBarSlotFull + 1) count = 32;
       if (i == Y::kBarSlotFree || i == Y::kBarSlotFree + 1) count = 2 + kSoftWarps;
       mbar_init(&bars[i], count);
@@ -235,8 +235,7 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       if (!advance_qk() || !advance_qk()) fail = true;
       for (; c >= 0 && !fail; c = ch.next(c + 1)) {
         const int st = nv % kNR;
-        if (!warp_wait(&bars[Y::kBarVFull + st], (nv / kNR) & 1) ||
-            !warp_wait(&bars[Y::kBarPFull + (nv & 1)], (nv >> 1) & 1)) {
+        if (!warp_wait(&bars[Y::kBarVFull + st], (nv / kNR) & 1)) {
           fail = true;
           break;
         }
@@ -258,8 +257,17 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const uint64_t vd = v_desc0 + (uint64_t)((st * Y::kStageBytes) >> 4);
         const uint32_t pcol = tbase + Y::kColS + (nv & 1) * kChunk;
 #pragma unroll
-        for (int kk = 0; kk < kChunk / 16; ++kk)
-          mma_ts_w(tbase, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        for (int step = 0; step < 2 && !fail; ++step) {
+          // a step brings 16 keys of each half of the chunk
+          if (!warp_wait(&bars[Y::kBarPFull + 2 * (nv & 1) + step], (nv >> 1) & 1)) fail = true;
+          tc_fence_after();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int kk = 2 * e + step;
+            mma_ts_w(tbase, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (!first || step > 0 || e > 0) ? 1u : 0u);
+          }
+        }
+        if (fail) break;
         first = false;
         mma_commit_w(&bars[Y::kBarVEmpty + st]);
         mma_commit_w(&bars[Y::kBarPVDone]);
@@ -395,22 +403,31 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           l *= alpha;
         }
         uint64_t acc[2] = {0, 0};
-        if (any) {
-          // a thread that sees none of its keys takes +inf as its reference: p = 0
-          const uint64_t negm2 = f2_splat(!kSel || part || lim ? -m_ref : -INFINITY);
-          if (part) p_quarter<false>(sv, lim, scale2, negm2, acc);
-          else p_quarter<true>(sv, 32, scale2, negm2, acc);
+        auto step_done = [&](int step) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[Y::kBarPFull + 2 * (n_all & 1) + step]);
+        };
+        // a thread that sees none of its keys takes +inf as its reference: p = 0
+        const uint64_t negm2 = f2_splat(!kSel || part || lim ? -m_ref : -INFINITY);
+        if (any && !part) {
+          p_quarter<true, 0, 16>(sv, 32, scale2, negm2, acc);
+          tmem_st8_split_of<16, 0>(s_col, sv);
+          p_quarter<true, 16, 24>(sv, 32, scale2, negm2, acc);  // beside the store
+          step_done(0);
+          p_quarter<true, 24, 32>(sv, 32, scale2, negm2, acc);
         } else {
-          zero_quarter(sv);
+          if (any) p_quarter<false>(sv, lim, scale2, negm2, acc);
+          else zero_quarter(sv);
+          tmem_st8_split_of<16, 0>(s_col, sv);
+          step_done(0);
         }
-        tmem_st16_split_lo<16>(s_col, sv);
+        tmem_st8_split_of<16, 8>(s_col + 8, sv);
         float sum0, sum1;
         f2_unpack(f2_add(acc[0], acc[1]), sum0, sum1);
         l += sum0 + sum1;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[Y::kBarPFull + (n_all & 1)]);
+        step_done(1);
         some = true;
         ++n_all;
       }

@@ -198,6 +198,13 @@ __device__ __forceinline__ void tmem_st16_split_lo(uint32_t taddr, const uint32_
       ::"r"(taddr), "n"(kSplit), QSA_W8(0), QSA_W8(8)
       : "memory");
 }
+// 16x32bx2 store of r[kFrom .. kFrom + 7] of a larger array (8 columns per thread).
+template <int kSplit, int kFrom>
+__device__ __forceinline__ void tmem_st8_split_of(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr),
+               "n"(kSplit), QSA_W8(kFrom)
+               : "memory");
+}
 #define QSA_WB8(i) "r"(b[i]), "r"(b[i + 1]), "r"(b[i + 2]), "r"(b[i + 3]), "r"(b[i + 4]), "r"(b[i + 5]), \
                    "r"(b[i + 6]), "r"(b[i + 7])
 // 16x32bx2 store of a[0..15] then b[0..15] (32 columns per thread).
