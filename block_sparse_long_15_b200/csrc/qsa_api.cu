@@ -658,6 +658,11 @@ qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, cons
   char *scratch = (char *)workspace + kStatusBytes;
   int *status = status_word(workspace);
   cudaStream_t st = (cudaStream_t)stream;
+#ifdef QSA_DEBUG
+  // debug build: check the selection the attention is about to read
+  if (sel)
+    if (cudaError_t e = launch_validate_paged_sel(D, G, sel, status, st)) return cuda_status(e);
+#endif
   // Sequences with many (token, head) rows go to the tensor-core kernel where it serves the shape,
   // the others to the row kernel; a single sequence to one of them.
   long long rows_below = 1LL << 62;

@@ -232,6 +232,9 @@ __device__ __forceinline__ PagedSeq paged_seq(const Paged &P, int b, int *status
   return s;
 }
 
+// launch_validate_sel for packed rows.
+cudaError_t launch_validate_paged_sel(const Dims &D, const Paged &P, const int32_t *sel, int *status, cudaStream_t st);
+
 // Norm + rotation of head rows (qsa_norm_rope) and the append (qsa_paged_append). A null
 // pos takes each row's position from the paged batch.
 struct NormRope {

@@ -379,7 +379,10 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
   Plan L;
   make_plan(P, smem + Y::kOffPlan, L);
   const int c = blockIdx.x;
-  if (c >= L.C) return;
+  if (c >= L.C) {
+    pdl_wait();
+    return;
+  }
   const long long lo = div_pos((long long)c * L.T, L.C), hi = div_pos((long long)(c + 1) * L.T, L.C);
 
   // ---- this warp's stream: iteration n is item lo + warp + kWarps n
@@ -580,6 +583,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
     i0 = i1;
   }
   cp_wait<0>();
+  // As a programmatic dependent of the chunk kernels it needs nothing of theirs, but it must not
+  // count as complete before they are.
+  pdl_wait();
 }
 
 // ---------------------------------------------------------------- any type and shape, CUDA cores
@@ -843,11 +849,12 @@ cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, cons
   P.min_items = 2 * kWarps;
   for (P.b0 = 0; P.b0 < G.batch; P.b0 += kMaxSeqs) {
     P.nb = min(kMaxSeqs, G.batch - P.b0);
+    const bool dep = pdl && P.b0 == 0;  // the launches of this loop share the workspace
     cudaError_t e;
     if (!mma) e = D.bf16 ? launch_simt<__nv_bfloat16>(P, st) : launch_simt<float>(P, st);
-    else if (D.d == 64) e = P.R == 8 ? launch_mma<64, 1>(P, st, pdl) : launch_mma<64, 2>(P, st, pdl);
-    else if (D.d == 128) e = P.R == 8 ? launch_mma<128, 1>(P, st, pdl) : launch_mma<128, 2>(P, st, pdl);
-    else e = P.R == 8 ? launch_mma<256, 1>(P, st, pdl) : launch_mma<256, 2>(P, st, pdl);
+    else if (D.d == 64) e = P.R == 8 ? launch_mma<64, 1>(P, st, dep) : launch_mma<64, 2>(P, st, dep);
+    else if (D.d == 128) e = P.R == 8 ? launch_mma<128, 1>(P, st, dep) : launch_mma<128, 2>(P, st, dep);
+    else e = P.R == 8 ? launch_mma<256, 1>(P, st, dep) : launch_mma<256, 2>(P, st, dep);
     if (e != cudaSuccess) {
       note_error("paged attention launch", e);
       return e;

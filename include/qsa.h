@@ -415,11 +415,13 @@ qsa_status_t qsa_paged_append(const qsa_config_t *cfg, const qsa_norm_rope_t *nr
                               const qsa_append_t *t, void *workspace, size_t workspace_bytes, qsa_stream_t stream);
 
 /* Bytes of workspace that qsa_paged_attn needs for this batch (the pointers of pg are
- * not read); the rules of qsa_workspace_size hold for it. */
+ * not read). The rules of qsa_workspace_size hold for it: it is all zero before its
+ * first use, and calls that share it do not overlap. It serves qsa_paged_attn and
+ * qsa_paged_append; the other entry points leave data where these expect zeros. */
 qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t *pg, size_t *bytes);
 
 /* Attention of the batch's new tokens over the paged cache, their own keys and values
- * included: q, out [n_tok][Hq][d] (dense). With sel NULL a row at position t attends
+ * included: q, out [n_tok][Hq][d] (dense, not overlapping). With sel NULL a row at position t attends
  * every token u <= t (a full-attention layer without the indexer). With sel [n_tok][k],
  * as qsa_index_score_topk writes it for the rows, it attends the listed blocks below
  * n_c(t) and its trailing range [n_c B, t], as in qsa_sparse_attn; a row that sees no

@@ -1,5 +1,8 @@
 """The paged-cache operators through the binding, against plain 64-bit forms (paged_util)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -473,6 +476,35 @@ def test_shared_prefix_pages(cuda_lib):
     s["g"]["page_table"][1, :2] = s["g"]["page_table"][0, :2]
     _attn(qsa, s)
     U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
+
+
+DEBUG_CHILD = r"""
+import torch
+from block_sparse_long_15_b200 import qsa
+from tests import test_paged_gpu as T
+assert qsa.LIB_PATH.endswith("libqsa_debug.so"), qsa.LIB_PATH
+s = T._run(qsa, ("bf16", 16, 2, 128, 64, 64, 3, [4, 0, 2], [700, 9, 120]))
+T._attn(qsa, s)
+assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_OK, "a valid selection was flagged"
+good = s["sel"].clone()  # packed row 1 is the first of sequence 0 (n_c = 10), row 6 the last of sequence 2 (n_c = 1)
+def swap(x): x[1, 0], x[1, 1] = good[1, 1], good[1, 0]
+def out_of_range(x): x[1, 2] = 10
+def early_end(x): x[1, 2] = -1
+def one_too_many(x): x[6, 1] = 0
+for spoil in (swap, out_of_range, early_end, one_too_many):
+    s["sel"].copy_(good)
+    spoil(s["sel"])
+    T._attn(qsa, s)
+    assert qsa.qsa_read_device_status(s["ws"]) == qsa.QSA_ERR_DEVICE_CHECK, spoil.__name__
+print("DEBUG_CHECKS_OK")
+"""
+
+
+def test_debug_build_checks_packed_selections(cuda_lib):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, QSA_LIBRARY="libqsa_debug.so", PYTHONPATH=root)
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD], cwd=root, env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "DEBUG_CHECKS_OK" in r.stdout, r.stdout + r.stderr
 
 
 # ------------------------------------------------------------------ a run of them together
