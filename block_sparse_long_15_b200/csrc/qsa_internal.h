@@ -219,11 +219,14 @@ struct PagedSeq {
   bool ok;
 };
 
+// Keys are counted in int32, up to the end of the last tile.
+constexpr int kMaxPagedLen = 0x7fffff00;
+
 // True geometry, or ok = false (and the device check recorded) when it does not fit.
 __device__ __forceinline__ PagedSeq paged_seq(const Paged &P, int b, int *status) {
   PagedSeq s;
   const int q0 = P.q_start[b], q1 = P.q_start[b + 1], len = P.kv_len[b];
-  s.ok = q0 >= 0 && q1 >= q0 && q1 <= P.n_tok && q1 - q0 <= P.max_chunk && len >= q1 - q0 &&
+  s.ok = q0 >= 0 && q1 >= q0 && q1 <= P.n_tok && q1 - q0 <= P.max_chunk && len >= q1 - q0 && len <= kMaxPagedLen &&
          (long long)len <= ((long long)P.max_pages << P.ps_shift);
   if (!s.ok) record_status(status, QSA_ERR_DEVICE_CHECK);
   s.q0 = q0;

@@ -62,7 +62,8 @@ constexpr int kBarPFull = kBarSFull + 2;        // [tile][step], 8 arrivals
 constexpr int kBarPVDone = kBarPFull + 4;       // [tile]
 constexpr int kBarSlotFull = kBarPVDone + 2;    // [slot], the builder's 32 lanes
 constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
-constexpr int kNumBars = kBarSlotFree + 2;
+constexpr int kBarDrain = kBarSlotFree + 2;     // every MMA of the block completed
+constexpr int kNumBars = kBarDrain + 1;
 static_assert(kNumBars * 8 <= 256, "barrier area");
 
 // A softmax thread's place: warp (tile w, lane group, sub-group) owns 16 rows of its tile; lane
@@ -220,6 +221,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+    // after a timeout, here or in another warp, copies may be in flight: they land before the block ends
+    for (int i = max(0, j - kNE); i < j; ++i) warp_wait(&bars[kBarFull + i % kNE], (i / kNE) & 1);
+    if (qn > 0) warp_wait(&bars[kBarQ], (qn - 1) & 1);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kChunk, false, false);
@@ -348,6 +352,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       record_status(P.status, QSA_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+    mma_commit_w(&bars[kBarDrain]);  // and MMAs complete
+    warp_wait(&bars[kBarDrain], 0);
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------- softmax + epilogue
     const int w = (warp - kSoftWarp0) >> 3;  // tile

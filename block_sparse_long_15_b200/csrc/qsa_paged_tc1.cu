@@ -61,7 +61,8 @@ struct Layout {
   static constexpr int kBarQEmpty = kBarQFull + 1;       // a phase per unit: its last QK completed
   static constexpr int kBarSlotFull = kBarQEmpty + 1;    // [slot], the builder's 32 lanes
   static constexpr int kBarSlotFree = kBarSlotFull + 2;  // [slot], producer + MMA warp + softmax warps
-  static constexpr int kNumBars = kBarSlotFree + 2;
+  static constexpr int kBarDrain = kBarSlotFree + 2;     // every MMA of the block completed
+  static constexpr int kNumBars = kBarDrain + 1;
   static_assert(kNumBars * 8 <= 512, "barrier area");
 };
 
@@ -121,7 +122,7 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     // no token there, or a page outside the pool) and loads its columns 64 e ..
     const int n_lanes = Y::kGroups * (kChunk / P.box), box_i = lane / Y::kGroups, e = lane % Y::kGroups;
     const uint32_t box_bytes = (uint32_t)P.box * 128;
-    int j = 0;  // chunks so far
+    int j = 0, jk = 0;  // chunks so far, and their K
     bool fail = false;
     for (int su = 0; !fail; ++su) {
       const int s = su & 1;
@@ -157,6 +158,7 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (lane == 0) mbar_arrive_expect_tx(&bars[Y::kBarKFull + st], bytes);
         __syncwarp();
         if (z >= 0) tma_load_3d(&tm_k, &bars[Y::kBarKFull + st], base + Y::kOffK + at, e * 64, y, z);
+        ++jk;
         if (j >= kNR && !warp_wait(&bars[Y::kBarVEmpty + st], ((j / kNR) & 1) ^ 1)) {
           fail = true;
           break;
@@ -176,6 +178,9 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       if (lane == 0) record_status(P.status, QSA_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+    // after a timeout, here or in another warp, copies may be in flight: they land before the block ends
+    for (int i = max(0, jk - kNR); i < jk; ++i) warp_wait(&bars[Y::kBarKFull + i % kNR], (i / kNR) & 1);
+    for (int i = max(0, j - kNR); i < j; ++i) warp_wait(&bars[Y::kBarVFull + i % kNR], (i / kNR) & 1);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kChunk, false, false);
@@ -286,6 +291,8 @@ k_paged_tc1(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       record_status(P.status, QSA_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+    mma_commit_w(&bars[Y::kBarDrain]);  // and MMAs complete
+    warp_wait(&bars[Y::kBarDrain], 0);
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------- softmax + epilogue
     // Warp (lane group, sub-group) owns 16 rows: thread t < 16 holds its row's first 32 keys of every

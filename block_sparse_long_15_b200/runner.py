@@ -166,6 +166,7 @@ class QSAPaged:
         self.kv_start = torch.zeros(slots, dtype=torch.int32, device=device)
         self.table = torch.zeros(slots, -(-max_len // page_size), dtype=torch.int32)
         self.length = [0] * slots
+        self.indexed = [0] * slots  # tokens with indexer keys
         self.pages = [[] for _ in range(slots)]
         self.free = list(range(n_pages - 1, -1, -1))
         self.ws = self.score_ws = None
@@ -173,7 +174,7 @@ class QSAPaged:
     def release(self, slot: int):
         """The slot's sequence has ended: its pages go back."""
         self.free += reversed(self.pages[slot])
-        self.pages[slot], self.length[slot] = [], 0
+        self.pages[slot], self.length[slot], self.indexed[slot] = [], 0, 0
         self.kbar_blocks[slot] = 0
 
     def reserve(self, counts):
@@ -212,9 +213,7 @@ class QSAPaged:
         padded = torch.zeros(self.slots, most, *qi.shape[1:], dtype=self.dtype, device=self.device)
         padded[seq, row] = qi
         sel = torch.empty(self.slots, most, qsa.qsa_topk_blocks(cfg), dtype=torch.int32, device=self.device)
-        need = qsa.qsa_workspace_size(cfg, qsa.QSA_PREFILL, self.slots, most, self.max_len)
-        if self.score_ws is None or self.score_ws.numel() < need:
-            self.score_ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        self.score_ws = self._grown(self.score_ws, qsa.qsa_workspace_size(cfg, qsa.QSA_PREFILL, self.slots, most, self.max_len))
         q_first = pg.kv_len - count.to(torch.int32).to(self.device)
         qsa.qsa_index_score_topk(cfg, padded, self.kbar_cache, pg.kv_len, q_first, self.max_len, sel, self.score_ws)
         return sel[seq, row].contiguous()
@@ -222,16 +221,28 @@ class QSAPaged:
     def step(self, counts, q, k, v, qi=None, ki=None):
         """counts[s] new tokens of every slot s, packed in that order: q [n_tok][Hq][d] and k, v
         [n_tok][Hkv][d] before norm and rotation. With the indexer's qi [n_tok][Hi][di] (rotated) and ki
-        [n_tok][di] the step attends the selected blocks. Returns [n_tok][Hq][d]."""
+        [n_tok][di] the step attends the selected blocks; a slot whose earlier tokens came without them
+        cannot. Returns [n_tok][Hq][d]."""
+        cfg, n = self.cfg, sum(counts)
+        heads, kv = (n, cfg.num_attention_heads, cfg.head_dim), (n, cfg.num_key_value_heads, cfg.head_dim)
+        want = [("q", q, heads), ("k", k, kv), ("v", v, kv)]
         if (qi is None) != (ki is None):
             raise ValueError("qi and ki come together")
+        if ki is not None:
+            want += [("qi", qi, (n, cfg.indexer_n_heads, cfg.indexer_head_dim)), ("ki", ki, (n, cfg.indexer_head_dim))]
+            for s, c in enumerate(counts):
+                if c and self.indexed[s] != self.length[s]:
+                    raise ValueError(f"slot {s}: {self.length[s]} tokens, {self.indexed[s]} of them with indexer keys")
+        for name, t, shape in want:  # before the lengths move
+            if tuple(t.shape) != shape or t.dtype != self.dtype:
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} {self.dtype}")
         self.reserve(counts)
-        if sum(counts) == 0:
+        if n == 0:
             return torch.empty_like(q)
         pg = self.batch(counts)
-        need = qsa.qsa_paged_workspace_size(self.cfg, pg)
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        self.ws = self._grown(self.ws, qsa.qsa_paged_workspace_size(self.cfg, pg))
+        if ki is not None:
+            self.indexed = [a + c for a, c in zip(self.indexed, counts)]
         turned, out = torch.empty_like(q), torch.empty_like(q)
         qsa.qsa_paged_append(self.cfg, self.nr, pg, k, v, self.k_pages, self.v_pages, self.ws, q=q, q_out=turned, ki=ki,
                              ki_cache=self.ki_cache if ki is not None else None)
@@ -239,6 +250,16 @@ class QSAPaged:
         qsa.qsa_paged_attn(self.cfg, pg, turned, self.k_pages, self.v_pages, sel, out, self.ws)
         return out
 
+    def _grown(self, ws, need: int):
+        """ws, or a larger one that keeps its status word."""
+        if ws is not None and ws.numel() >= need:
+            return ws
+        new = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        if ws is not None:
+            new[:256] = ws[:256]
+        return new
+
     def status(self) -> int:
         """First device status of the steps since the last reading (QSA_OK before the first step)."""
-        return qsa.QSA_OK if self.ws is None else qsa.qsa_read_device_status(self.ws)
+        codes = [qsa.qsa_read_device_status(ws) for ws in (self.ws, self.score_ws) if ws is not None]
+        return next((c for c in codes if c != qsa.QSA_OK), qsa.QSA_OK)

@@ -335,7 +335,7 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
  * q_start[b + 1] - 1 of every packed tensor, and with n = q_start[b + 1] -
  * q_start[b], row q_start[b] + i sits at position t = kv_len[b] - n + i. A sequence
  * may have no new token. Rows before q_start[0] and from q_start[batch] on belong to
- * no sequence: they are not read and nothing is written for them.
+ * no sequence: what they hold does not matter and nothing is written for them.
  *
  * Pages: k_pages, v_pages [n_pages][Hkv][page_size][d]. Token u of sequence b sits in
  * slot u % page_size of page page_table[b][u / page_size]; entries behind a
@@ -345,7 +345,7 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
  * earlier tokens of the same chunk, though not another sequence.
  *
  * A sequence whose geometry does not fit (q_start that falls or passes n_tok, more
- * new tokens than max_chunk or kv_len, kv_len beyond max_pages * page_size) or that
+ * new tokens than max_chunk or kv_len, kv_len beyond max_pages * page_size or 2^31 - 256) or that
  * needs a page outside [0, n_pages) records QSA_ERR_DEVICE_CHECK in the workspace
  * status word; nothing out of range is read or written for it, its own rows and
  * slots are unspecified, and the other sequences are served (where q_start falls, the

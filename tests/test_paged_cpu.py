@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from block_sparse_long_15_b200 import build
 
@@ -177,3 +178,26 @@ def test_page_bookkeeping(qsa):
     assert sorted(r.free + sum(r.pages, [])) == list(range(6))
     with pytest.raises(ValueError):
         r.step([0, 0, 1], None, None, None, qi=None, ki=1)
+
+
+def test_a_refused_step_changes_nothing(qsa):
+    """A step whose tensors do not fit, or that selects over tokens without indexer keys, is refused
+    before any length or page moves."""
+    from block_sparse_long_15_b200.runner import QSAPaged
+    cfg = _cfg(qsa)
+    r = QSAPaged(cfg, slots=2, max_len=256, n_pages=8, page_size=64, device="cpu")
+    r.reserve([64, 0])  # tokens that came without indexer keys
+    before = ([list(p) for p in r.pages], list(r.length), list(r.indexed), list(r.free))
+
+    def rows(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype)
+    good = dict(q=rows(3, 16, 128), k=rows(3, 2, 128), v=rows(3, 2, 128))
+    index = dict(qi=rows(3, 4, 64), ki=rows(3, 64))
+    bad = [(dict(good, q=rows(2, 16, 128)), [0, 3]), (dict(good, k=rows(3, 4, 128)), [0, 3]),
+           (dict(good, v=rows(3, 2, 128, dtype=torch.float32)), [0, 3]), (dict(good, **dict(index, ki=None)), [0, 3]),
+           (dict(good, **dict(index, qi=rows(3, 4, 128))), [0, 3]), (dict(good, **dict(index, ki=rows(3, 32))), [0, 3]),
+           (dict(good, **index), [3, 0]), (good, [300, -297])]
+    for kw, counts in bad:
+        with pytest.raises((ValueError, TypeError)):
+            r.step(counts, **kw)
+        assert ([list(p) for p in r.pages], list(r.length), list(r.indexed), list(r.free)) == before, (counts, kw.keys())

@@ -478,6 +478,38 @@ def test_shared_prefix_pages(cuda_lib):
     U.check(s["out"][s["rows"]], *_oracle(s, case), "out")
 
 
+def test_lengths_at_the_end_of_int32_are_refused(cuda_lib):
+    """Keys are counted in int32 up to the end of a tile: a longer sequence is refused, its neighbours are
+    served. (Its table names one page over and over; the table itself is long enough.)"""
+    qsa = cuda_lib
+    case = ("bf16", 8, 2, 128, 32768, 64, 0, [1, 1], [40, 70])
+    s = _run(qsa, case, lead=0, tail=0)
+    want, tol = _oracle(s, case)
+    table = torch.zeros(2, 65536, dtype=torch.int32)
+    table[:, :1] = s["g"]["page_table"].cpu()[:, :1]
+    for length in (2**31 - 1, 2**31 - 255):
+        g = dict(s["g"], page_table=table.cuda(), kv_len=torch.tensor([length, 70], dtype=torch.int32).cuda())
+        pg = qsa.make_paged(**g)
+        ws = qsa.alloc_paged_workspace(s["cfg"], pg)
+        qsa.qsa_paged_attn(s["cfg"], pg, s["q"], s["kp"], s["vp"], None, s["out"], ws)
+        assert qsa.qsa_read_device_status(ws) == qsa.QSA_ERR_DEVICE_CHECK
+        U.check(s["out"][1:], want[1:], tol[1:], f"beside {length}")
+
+
+def test_status_survives_a_larger_workspace(cuda_lib):
+    """A recorded status is still there when a later step needs a larger workspace."""
+    from block_sparse_long_15_b200.runner import QSAPaged
+    qsa = cuda_lib
+    run = QSAPaged(qsa.make_config(16, 2, 128, 4, 64, 64, 4, "bf16"), slots=1, max_len=640, n_pages=10, page_size=64)
+    rows = lambda n: [torch.zeros(n, h, 128, dtype=torch.bfloat16, device="cuda") for h in (16, 2, 2)]
+    run.step([1], *rows(1))
+    small = run.ws
+    small[:4].view(torch.int32)[0] = qsa.QSA_ERR_DEVICE_CHECK
+    run.step([200], *rows(200))
+    assert run.ws is not small, "the larger chunk needs the tensor-core kernel's partials"
+    assert run.status() == qsa.QSA_ERR_DEVICE_CHECK and run.status() == qsa.QSA_OK
+
+
 DEBUG_CHILD = r"""
 import torch
 from block_sparse_long_15_b200 import qsa
