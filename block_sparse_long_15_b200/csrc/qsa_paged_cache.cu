@@ -28,9 +28,12 @@
 namespace qsa {
 namespace {
 
-constexpr int kWarps = 4;
-// Warp rows in flight per warp: 16K rows of 32 + 4 heads of 128 take 61 us with 4, 57 with 6, 59
-// with 8; more warps with fewer registers each (8 or 10 blocks an SM) 61 to 68.
+// Blocks of one warp: a warp that ends makes room for the next at once (blocks of four: 78 us instead
+// of 72 to append 16K tokens, 58 instead of 56 for 16K rows of 32 + 4 heads of 128).
+constexpr int kThreads = 32;
+// Warp rows in flight per warp: those 16K rows take 61 us with 4, 57 with 6, 59 with 8; more warps with
+// fewer registers each 61 to 68. Several tokens a warp, with the positions looked up for all of
+// them at once: 65 to 73; a token's rows over two or three warps: 66 and 69.
 constexpr int kBatch = 6;
 constexpr int kMaxHalf = 128;   // rotary pairs of a head: head_dim <= 256
 constexpr long long kFillWarps = 148 * 32;
@@ -219,13 +222,12 @@ __device__ __forceinline__ void run_rows(const Rows<T> &w, const Place &p, const
 
 // kD: the head dim, 0 for one without an instantiation of its own
 template <typename T, bool kPaged, int kD>
-__global__ void __launch_bounds__(kWarps * 32) k_norm_rope(const __grid_constant__ NrParams P) {
+__global__ void __launch_bounds__(kThreads) k_norm_rope(const __grid_constant__ NrParams P) {
   using namespace sm100;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x;
   // warp `part` of token n
-  const unsigned g = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const unsigned g = blockIdx.x;
   const int n = P.parts == 1 ? (int)g : (int)(g / (unsigned)P.parts), part = P.parts == 1 ? 0 : (int)(g % (unsigned)P.parts);
-  if (n >= P.n_tok) return;
   const AppendArgs &A = P.A;
 
   // warp rows: those of q, then k, v and the indexer key
@@ -416,8 +418,8 @@ cudaError_t launch(const Dims &D, const NormRope &N, NrParams &P, cudaStream_t s
   P.nk = P.A.k ? (D.Hkv + per - 1) / per : 0;
   P.n_rows = P.nq + P.nk * (P.pos ? 1 : 2) + (P.A.ki ? 1 : 0);
   P.parts = (int)std::max(1LL, std::min((long long)P.n_rows, kFillWarps / P.n_tok));
-  const long long blocks = ((long long)P.n_tok * P.parts + kWarps - 1) / kWarps;
-  if (blocks * kWarps > 0xffffffffLL) return cudaErrorNotSupported;
+  const long long blocks = (long long)P.n_tok * P.parts;
+  if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
   note_launch();
   auto pick = [&](auto d) {
     constexpr int kD = decltype(d)::value;
@@ -428,7 +430,7 @@ cudaError_t launch(const Dims &D, const NormRope &N, NrParams &P, cudaStream_t s
               : D.d == 128 ? pick(std::integral_constant<int, 128>{})
               : D.d == 256 ? pick(std::integral_constant<int, 256>{})
                            : pick(std::integral_constant<int, 0>{});
-  kern<<<(unsigned)blocks, kWarps * 32, 0, st>>>(P);
+  kern<<<(unsigned)blocks, kThreads, 0, st>>>(P);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) note_error("k_norm_rope launch", e);
   return e;
