@@ -3,8 +3,10 @@
 // Every head x of d elements at position t becomes
 //   y = x / sqrt(mean(x^2) + eps) * (w + w_off),  then for i < r/2, j = i + r/2:
 //   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a),  a = t theta^(-2i/r),
-// in fp32, rounded once. Each element is read once and written once, with about 7
-// operations between: bound by HBM for a prompt, by latency for a decode step.
+// in fp32, rounded once. Each element is read once and written once, with about 7 operations
+// between: bound by HBM for a prompt (16K tokens, 32 + 4 heads of 128 in bf16, 302 MB: 56 us,
+// 5.4 TB/s; appending as many, 330 MB with 256-byte pieces going to the pages: 72 us, 4.6 TB/s),
+// by latency for a decode step (64 tokens: 3 us, 4 with the append).
 //
 // A warp takes the heads of one token (or, with few tokens, a part of them: each of them then
 // computes the token's angles again). A head of d elements sits in d / 8 lanes, so a warp

@@ -379,6 +379,8 @@ __device__ __forceinline__ void build_segments(const TcParams &P, const SlotArea
 // later ones, 128 elements of each from 128 z on, a row a warp. Lane p holds the statistics of part
 // p, so that all parts' rows can be read at once:
 //   out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
+// 7 us behind 148 CTAs. (With the plan made again in every block and the parts read one after the
+// other it took 21 to 30.)
 constexpr int kMergeWarps = 16, kMergeRows = kMergeWarps;
 template <class X>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {

@@ -25,6 +25,11 @@
 // in the 16-row operand, the 8 heads of a group fill the 8 columns, where S = Q K^T would
 // leave half of the rows empty. P^T turns from accumulator to operand layout with one
 // movmatrix per 8 x 8.
+//
+// Measured, 16 / 2 heads of 128, pages of 64: 64 sequences of 4K .. 32K tokens (1.24 GB) 199 us, 6.2 TB/s;
+// over 32 selected blocks each (137 MB) 33 us in a graph, of which the chain of length, list entry, page
+// number and first tile takes 6 and the merge of units that CTAs share 2 to 6; one sequence of
+// 1500 tokens 12 us, latency throughout.
 #include <math.h>
 
 #include <algorithm>
@@ -593,7 +598,8 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
 // tiles at a time for the whole CTA. Lanes are keys for the logits and dims for the output;
 // everything in fp32. Latency bounds it (a selection, a page table and the keys, one after the
 // other): the pool rows of up to 32 tiles are looked up at once, the rows are dealt out to the warps
-// one by one, and several CTAs share an SM.
+// one by one, and several CTAs share an SM. 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32,
+// 4 / 1 heads of 64 in fp32: 46 us. 64 keys a step instead of 32 took longer (fewer CTAs an SM).
 constexpr int kLookTiles = 32;
 constexpr int kSimtKeys = 2 * kTile;
 

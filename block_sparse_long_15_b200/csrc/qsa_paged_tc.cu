@@ -18,12 +18,21 @@
 //   warp 1      MMA issuer (TMEM owner): per chunk O_A += P_A V, S_A = Q_A K'^T, then B;
 //   warp 2      builder: the next unit's geometry, selection lists and chunk bitmaps;
 //   warps 4-19  softmax, eight per tile, 16 rows per warp, two threads a row with 64 logits
-//               each in registers (16x32bx2 TMEM accesses): row max by one shuffle, P in bf16
-//               over the first half of each S half, in two steps that the PV product takes
-//               as they come, O rescaled only when the max has moved by more than 2^8, and
-//               the epilogue. Four warps a scheduler: with one thread a row the exponentials
-//               and the arithmetic around them did not overlap (1560-1610 us at 8K of 32K).
+//               each, 32 in registers at a time (16x32bx2 TMEM accesses): row max by one
+//               shuffle, P in bf16 over the first half of each S half, in two steps that the
+//               PV product takes as they come, O rescaled only when the max has moved by more
+//               than 2^8, and the epilogue. Four warps a scheduler: with one thread a row the
+//               exponentials and the arithmetic around them did not overlap (1560-1630 us at
+//               8K of 32K tokens).
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
+//
+// Measured, 16 / 2 heads, pages of 64: 8192 tokens of 32768 1530 us alone (1.26 PFLOP/s, 0.77 of
+// cuBLAS), 1780 in long loops under the power cap; tensor pipe 60 % busy, MUFU 62 %. A part of the
+// exponentials as polynomials on the FMA pipe: no gain, the issue slots are as scarce. 4096 tokens of
+// 24000, 64 independently selected blocks each: 665 us, in which 16 tokens see nearly every
+// block between them and the products of the whole context are made (0.74 PFLOP, 1.1 PFLOP/s). The
+// row kernel, which reads every token's own blocks, is bound by L2 there (1535 us). Products per
+// 64-key half that a tile sees: 675 to 775 us, the shorter MMAs save less than their issue costs.
 #include "qsa_paged_plan.cuh"
 
 namespace qsa {
