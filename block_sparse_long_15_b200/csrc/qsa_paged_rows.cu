@@ -33,7 +33,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "qsa_internal.h"
 #include "sm100_ptx.cuh"
@@ -221,12 +220,12 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v
 
 __device__ __forceinline__ float weight_of(float m, float m_max) { return m == -INFINITY ? 0.f : ex2_approx(m - m_max); }
 
-// The CTA's items [i0, i1) of unit u are done: NB buffers buf[w] ([R][d] fp32, swizzled where
-// warps have one each) with their wm / wl hold them. A whole unit is written out; a part goes to
-// the CTA's slot. Ends with a barrier.
-template <typename T, int NB>
+// The CTA's items [i0, i1) of unit u are done: the warps' buffers buf[w] ([R][d] fp32, swizzled or not)
+// with their wm / wl hold them. A whole unit is written out; a part goes to the CTA's slot. Ends
+// with a barrier.
+template <typename T, bool kSwz>
 __device__ __forceinline__ void finish_segment(const RowsParams &P, const Plan &L, const Unit &u, long long i0, long long i1,
-                                               long long lo, float *const (&buf)[NB], const float *wm, const float *wl) {
+                                               long long lo, float *const (&buf)[kWarps], const float *wm, const float *wl) {
   const int d = P.d, R = P.R, d4 = d >> 2;
   const int c = blockIdx.x;
   const bool whole = i0 == u.first && i1 == u.end;
@@ -236,13 +235,13 @@ __device__ __forceinline__ void finish_segment(const RowsParams &P, const Plan &
     const int r = e / d4, c4 = (e - r * d4) * 4;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NB; ++w) m = fmaxf(m, wm[w * kMaxRows + r]);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, wm[w * kMaxRows + r]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll
-    for (int w = 0; w < NB; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float f = weight_of(wm[w * kMaxRows + r], m);
-      const float4 x = *(const float4 *)(buf[w] + r * d + (NB > 1 ? swz(r, c4) : c4));
+      const float4 x = *(const float4 *)(buf[w] + r * d + (kSwz ? swz(r, c4) : c4));
       o.x = fmaf(f, x.x, o.x);
       o.y = fmaf(f, x.y, o.y);
       o.z = fmaf(f, x.z, o.z);
@@ -583,7 +582,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
       const int nw = left > 0 ? (int)((left + kWarps - 1) / kWarps) : 0;
       buf[w] = (float *)(smem + w * Y::kWarpBytes + ((nw + S - 1) % S) * Y::kStageBytes);
     }
-    finish_segment<__nv_bfloat16, kWarps>(P, L, u, i0, i1, lo, buf, wm, wl);
+    finish_segment<__nv_bfloat16, true>(P, L, u, i0, i1, lo, buf, wm, wl);
     settle<__nv_bfloat16>(P, L, u, i0, i1);
     i0 = i1;
   }
@@ -594,14 +593,38 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- any type and shape, CUDA cores
-// fp32, and bf16 head widths or block sizes without a tensor-core form: the same items, two
-// tiles at a time for the whole CTA. Lanes are keys for the logits and dims for the output;
-// everything in fp32. Latency bounds it (a selection, a page table and the keys, one after the
-// other): the pool rows of up to 32 tiles are looked up at once, the rows are dealt out to the warps
-// one by one, and several CTAs share an SM. 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32,
-// 4 / 1 heads of 64 in fp32: 46 us. 64 keys a step instead of 32 took longer (fewer CTAs an SM).
-constexpr int kLookTiles = 32;
-constexpr int kSimtKeys = 2 * kTile;
+// fp32, and bf16 head widths or block sizes without a tensor-core form: the same items and streams with
+// units of R = 4 or 8 rows, everything in fp32. A warp holds all rows of the unit against the 16 keys
+// of its tile, so that K and V are read from shared memory once for the R rows: lanes are
+// (key, half of the dims) for the logits, whose weights then go through shared memory to lanes that are dims
+// (and, up to 64 dims, halves of the keys). The ring holds K and V of a tile as entries of their own (of up
+// to 512 bytes a row: two each at 256 dims in fp32).
+// Measured in fp32: 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32, 4 / 1 heads of 64, 26 us, latency; a
+// step of 64 sequences of 2K .. 8K, 16 / 2 heads of 128, 160 us (4.1 TB/s); 4 chunks of 450 tokens of 2000, 1466 us
+// (17.7 TFLOP/s: shared memory, and the softmax between the products). With 32 keys a step for the whole CTA and
+// barriers around each they took 46, 371 and 1673.
+template <typename T, int R, int kD_>
+struct SimtLayout {
+  static constexpr int kElems = 16 / sizeof(T);  // elements of 16 bytes
+  static constexpr int kPart = kD_ * sizeof(T) <= 512 ? kD_ : 512 / sizeof(T), kParts = kD_ / kPart;  // dims of an entry
+  static constexpr uint32_t kRowBytes = kPart * sizeof(T), kEntryBytes = kTile * kRowBytes;
+  // Few entries and many warps: at 128 dims in fp32 two entries and three CTAs an SM take 1466 us where three
+  // entries and two CTAs take 1873 (four chunks of 450 tokens of 2000, 16 / 2 heads), at 64 dims three
+  // and four take 27 us where four and three take 29 (the small case above).
+  // Few entries and many warps: the logits and the softmax of a tile are one chain, which other warps cover. In
+  // fp32, four chunks of 450 tokens of 2000, 16 / 2 heads: at 128 dims two entries and three CTAs an SM
+  // 1466 us, three and two 1873; at 256 dims 3088 and 3552.
+  static constexpr int kEntries = kRowBytes <= 256 ? 3 : 2;
+  static constexpr int kCtas = kRowBytes <= 256 ? 4 : 3;  // per SM
+  static constexpr uint32_t kWarpBytes = kEntries * kEntryBytes;
+  static constexpr uint32_t kOffMeta = kWarps * kWarpBytes;            // [warp][4] key0, nv
+  static constexpr uint32_t kOffMl = kOffMeta + kWarps * 4 * 8;        // wm, wl [warp][kMaxRows]
+  static constexpr uint32_t kOffQ = kOffMl + 2 * kWarps * kMaxRows * 4;  // [R][kD_] fp32
+  static constexpr uint32_t kOffP = kOffQ + R * kD_ * 4;               // [warp][key][R] fp32
+  static constexpr uint32_t kOffPlan = kOffP + kWarps * kTile * R * 4;
+  // a free entry holds a warp's fp32 output while its segment is merged
+  static_assert(R * kD_ * 4 <= kEntryBytes, "merge buffer");
+};
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
@@ -614,174 +637,235 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-// One step of a warp: its first N rows (qs, kWarps d apart) against the 32 keys in shared memory; lane
-// `key` is the key's position, beyond every row's where nobody sees it.
-constexpr int kRW = kMaxRows / kWarps;  // rows per warp
-template <int N, bool kHi>  // kHi: d > 128, a second group of dims
-__device__ __forceinline__ void simt_step(const float *ks, const float *vs, const float *qs, int d, int key,
-                                          const int (&trow)[kRW], float sl2, float (&m)[kRW], float (&l)[kRW],
-                                          float4 (&o)[kRW][2]) {
-  const int lane = threadIdx.x & 31;
-  float acc[N], p[N];
-#pragma unroll
-  for (int r = 0; r < N; ++r) acc[r] = 0.f;
-  const float *kr = ks + lane * (d + 4);
-#pragma unroll 4
-  for (int c4 = 0; c4 < d; c4 += 4) {
-    const float4 x = *(const float4 *)(kr + c4);
-#pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float4 y = *(const float4 *)(qs + r * kWarps * d + c4);
-      acc[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[r]))));
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < N; ++r) {
-    const float x = key <= trow[r] ? acc[r] * sl2 : -INFINITY;
-    float mx = x;
-#pragma unroll
-    for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float mn = fmaxf(m[r], mx);
-    const float f = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
-    p[r] = x == -INFINITY ? 0.f : ex2_approx(x - mn);
-    l[r] = fmaf(l[r], f, p[r]);
-    m[r] = mn;
-#pragma unroll
-    for (int q = 0; q < (kHi ? 2 : 1); ++q) {
-      o[r][q].x *= f;
-      o[r][q].y *= f;
-      o[r][q].z *= f;
-      o[r][q].w *= f;
-    }
-  }
-  const bool lo = lane * 4 < d, hi = 128 + lane * 4 < d;  // the lane's two groups of four dims
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 x = lo ? *(const float4 *)(vs + k * d + lane * 4) : zero;
-    const float4 y = kHi && hi ? *(const float4 *)(vs + k * d + 128 + lane * 4) : zero;
-#pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float pk = __shfl_sync(0xffffffffu, p[r], k);
-      o[r][0].x = fmaf(pk, x.x, o[r][0].x);
-      o[r][0].y = fmaf(pk, x.y, o[r][0].y);
-      o[r][0].z = fmaf(pk, x.z, o[r][0].z);
-      o[r][0].w = fmaf(pk, x.w, o[r][0].w);
-      if (kHi) {
-        o[r][1].x = fmaf(pk, y.x, o[r][1].x);
-        o[r][1].y = fmaf(pk, y.y, o[r][1].y);
-        o[r][1].z = fmaf(pk, y.z, o[r][1].z);
-        o[r][1].w = fmaf(pk, y.w, o[r][1].w);
-      }
-    }
-  }
-}
-
-size_t simt_fixed_bytes(int d) {  // K, V, q, O of the CTA
-  return sizeof(float) * ((size_t)kSimtKeys * (2 * d + 4) + 2 * (size_t)kMaxRows * (d + 1));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) k_paged_simt(const __grid_constant__ RowsParams P, int fixed) {
+template <typename T, int R, int kD_>
+__global__ void __launch_bounds__(kThreads, SimtLayout<T, R, kD_>::kCtas) k_paged_simt(const __grid_constant__ RowsParams P) {
+  typedef SimtLayout<T, R, kD_> Y;
+  constexpr int N = Y::kEntries, kElems = Y::kElems, kChunks = Y::kRowBytes / 16;
+  constexpr int kPart = Y::kPart, kParts = Y::kParts, kPer = 2 * kParts;  // entries per tile
+  constexpr int kGroups = kD_ == 256 ? 2 : 1, kIn = kGroups / kParts;     // groups of four dims of a lane in O, in an entry
+  constexpr bool kSplit = kD_ == 64;           // 16 lanes hold O: the two halves of a warp take every other key
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_key0[kLookTiles];
-  __shared__ long long s_row[kLookTiles * kTile];  // pool row of a key, -1: nobody sees it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int d = P.d, d4 = d >> 2;
-  float *ks = (float *)smem;            // [32][d + 4]
-  float *vs = ks + kSimtKeys * (d + 4); // [32][d]
-  float *qs = vs + kSimtKeys * d;       // [R][d]
-  float *os = qs + kMaxRows * d;       // [R][d]
-  float *wm = os + kMaxRows * d, *wl = wm + kMaxRows;
+  const int d = P.d;
+  auto chunks_of = [&](int part) { return min(kChunks, d / kElems - part * kChunks); };  // 16-byte pieces of a row
+  uint8_t *ring = smem + warp * Y::kWarpBytes;
+  int2 *meta = (int2 *)(smem + Y::kOffMeta) + warp * 4;
+  float *wm = (float *)(smem + Y::kOffMl), *wl = wm + kWarps * kMaxRows;
+  float *qs = (float *)(smem + Y::kOffQ), *ps = (float *)(smem + Y::kOffP) + warp * kTile * R;
+
   Plan L;
-  make_plan(P, smem + fixed, L);
+  make_plan(P, smem + Y::kOffPlan, L);
   const int c = blockIdx.x;
   if (c >= L.C) return;
   const long long lo = div_pos((long long)c * L.T, L.C), hi = div_pos((long long)(c + 1) * L.T, L.C);
 
+  // ---- this warp's stream: iteration n is item lo + warp + kWarps n, entries kPer n .. (K) and kPer n + kParts .. (V)
+  long long row_l = 0, next_l = 0;  // lane l: of iteration 32 (n / 32) + l the pool row of the first key, and of
+  int key_l = 0, nv_l = 0, cut_l = kTile;  // key `cut`, the first one in another page; first key and key count
+  auto prefetch = [&](int h) {
+    const int n = h / kPer, j = h % kPer, part = j % kParts;
+    if (j == 0 && (n & 31) == 0) {
+      const long long i = lo + warp + (long long)kWarps * (n + lane);
+      nv_l = 0;
+      row_l = next_l = 0;
+      key_l = 0;
+      cut_l = kTile;
+      if (i < hi) {
+        const Unit u = unit_of(P, L, i);
+        tile_keys(P, u, (int)(i - u.first), key_l, nv_l);
+        if (nv_l > 0) {
+          const int in_page = P.P.ps - (key_l & (P.P.ps - 1));
+          row_l = key_row(P, u, key_l);
+          if (row_l < 0) row_l = 0, nv_l = 0;
+          if (in_page < nv_l) {
+            cut_l = in_page;
+            next_l = key_row(P, u, key_l + in_page);
+            if (next_l < 0) next_l = 0, nv_l = in_page;
+          }
+        }
+      }
+    }
+    const long long row = __shfl_sync(0xffffffffu, row_l, n & 31), next = __shfl_sync(0xffffffffu, next_l, n & 31);
+    const int key0 = __shfl_sync(0xffffffffu, key_l, n & 31), nv = __shfl_sync(0xffffffffu, nv_l, n & 31);
+    const int cut = __shfl_sync(0xffffffffu, cut_l, n & 31);
+    if (lane == 0) meta[n & 3] = make_int2(key0, nv);
+    if (lo + warp + (long long)kWarps * n < hi) {
+      const uint32_t dst = smem_u32(ring + h % N * Y::kEntryBytes);
+      const T *pool = (const T *)(j < kParts ? P.kp : P.vp);
+      const int chunks = chunks_of(part);
+#pragma unroll
+      for (int e0 = 0; e0 < kTile * kChunks; e0 += 32) {
+        const int e = e0 + lane, r = e / kChunks, q = e % kChunks;
+        if (q >= chunks) continue;
+        const int take = r < nv ? 16 : 0;  // keys that nobody sees are zero
+        const T *src = take ? pool + (r < cut ? row + r : next + (r - cut)) * d + part * kPart + q * kElems : pool;
+        cp16(dst + r * Y::kRowBytes + ((q ^ (r & 7)) << 4), src, take);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int h = 0; h < N - 1; ++h) prefetch(h);
+
+  int n = 0;  // iterations done
   for (long long i0 = lo; i0 < hi;) {
     const Unit u = unit_of(P, L, i0);
     const long long i1 = min(hi, u.end);
-    for (int e = threadIdx.x; e < P.R * d4; e += kThreads) {
-      const int r = e / d4, c4 = (e - r * d4) * 4;
+    for (int e = threadIdx.x; e < R * (d >> 2); e += kThreads) {
+      const int r = e / (d >> 2), c4 = (e - r * (d >> 2)) * 4;
       int tok, h;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (unit_row(P, u, r, tok, h)) x = load4((const T *)P.q + ((size_t)(u.s.q0 + tok) * P.Hq + u.g * P.G + h) * d + c4);
-      *(float4 *)(qs + r * d + c4) = x;
+      *(float4 *)(qs + r * kD_ + c4) = x;
     }
-    int trow[kRW], n_mine = 0;  // row r of the warp is row kWarps r + warp of the unit; valid ones come first
-    float m[kRW], l[kRW];
-    float4 o[kRW][2];
-#pragma unroll
-    for (int r = 0; r < kRW; ++r) {
+    int trow[R];  // positions of the rows
+    {
       int tok, h;
-      const bool in = unit_row(P, u, r * kWarps + warp, tok, h);
-      trow[r] = in ? u.s.len - u.s.n + tok : -1;
-      if (in) n_mine = r + 1;
+      const int t = unit_row(P, u, lane, tok, h) ? u.s.len - u.s.n + tok : -1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) trow[r] = __shfl_sync(0xffffffffu, t, r);
+    }
+    float m[R], l[R];
+    float4 o[R][kGroups];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
-      o[r][0] = o[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (long long i = i0; i < i1; i += 2) {
-      const int look = (int)(i - i0) % kLookTiles;
-      __syncthreads();
-      if (look == 0) {
-        const int n_look = (int)min((long long)kLookTiles, i1 - i);
-        for (int e = threadIdx.x; e < kLookTiles * kTile; e += kThreads) {
-          int key0 = 0, nv = 0;
-          if (e / kTile < n_look) tile_keys(P, u, (int)(i - u.first) + e / kTile, key0, nv);
-          s_row[e] = e % kTile < nv ? key_row(P, u, key0 + e % kTile) : -1;
-          if (e % kTile == 0) s_key0[e / kTile] = key0;
-        }
-        __syncthreads();
-      }
-      const long long *rows = s_row + look * kTile;
-      for (int e = threadIdx.x; e < kSimtKeys * d4; e += kThreads) {
-        const int kk = e / d4, c4 = (e - kk * d4) * 4;
-        const long long row = rows[kk];
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (row >= 0) {
-          x = load4((const T *)P.kp + (size_t)row * d + c4);
-          y = load4((const T *)P.vp + (size_t)row * d + c4);
-        }
-        *(float4 *)(ks + kk * (d + 4) + c4) = x;
-        *(float4 *)(vs + kk * d + c4) = y;
-      }
-      __syncthreads();
-      if (n_mine == 0) continue;
-      const int key = rows[lane] >= 0 ? s_key0[look + lane / kTile] + lane % kTile : 0x7fffffff;
-      auto step = [&](auto n, auto hi) {
-        simt_step<decltype(n)::value, decltype(hi)::value>(ks, vs, qs + warp * d, d, key, trow, P.sl2, m, l, o);
-      };
-      auto pick = [&](auto hi) {
-        if (n_mine == 1) step(std::integral_constant<int, 1>{}, hi);
-        else if (n_mine == 2) step(std::integral_constant<int, 2>{}, hi);
-        else if (n_mine == 3) step(std::integral_constant<int, 3>{}, hi);
-        else step(std::integral_constant<int, 4>{}, hi);
-      };
-      if (d > 128) pick(std::true_type{});
-      else pick(std::false_type{});
-    }
 #pragma unroll
-    for (int r = 0; r < kRW; ++r) {
-      const int row = r * kWarps + warp;
+      for (int g = 0; g < kGroups; ++g) o[r][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();  // the queries are there
+
+    for (; lo + warp + (long long)kWarps * n < i1; ++n) {
+      const int key = lane & 15;
+      int2 kn;
+      float acc[R];
 #pragma unroll
-      for (int s = 16; s; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
+      for (int r = 0; r < R; ++r) acc[r] = 0.f;
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const int h = kPer * n + part;
+        __syncwarp();  // every lane is done with the entry that is filled next
+        prefetch(h + N - 1);
+        cp_wait<N - 1>();
+        __syncwarp();
+        kn = meta[n & 3];
+        if (kn.y == 0) continue;
+        const uint8_t *kr = ring + h % N * Y::kEntryBytes + key * Y::kRowBytes;
+        const int chunks = chunks_of(part);
+#pragma unroll 2
+        for (int q = lane >> 4; q < chunks; q += 2) {
+          const T *at = (const T *)(kr + ((q ^ (key & 7)) << 4));
+#pragma unroll
+          for (int e = 0; e < kElems; e += 4) {
+            const float4 x = load4(at + e);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float4 y = *(const float4 *)(qs + r * kD_ + part * kPart + q * kElems + e);
+              acc[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc[r]))));
+            }
+          }
+        }
+      }
+      if (kn.y > 0) {
+        float p[R], fix[R];
+        bool moved = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], 16);
+          const float x = key < kn.y && kn.x + key <= trow[r] ? acc[r] * P.sl2 : -INFINITY;
+          float mx = x;
+#pragma unroll
+          for (int s = 8; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          const float mn = fmaxf(m[r], mx);
+          fix[r] = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
+          moved |= mn != m[r];
+          p[r] = x == -INFINITY ? 0.f : ex2_approx(x - mn);
+          l[r] = fmaf(l[r], fix[r], p[r]);
+          m[r] = mn;
+        }
+        if (lane < kTile)
+#pragma unroll
+          for (int r = 0; r < R; r += 4) *(float4 *)(ps + lane * R + r) = make_float4(p[r], p[r + 1], p[r + 2], p[r + 3]);
+        if (__any_sync(0xffffffffu, moved))
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) o[r][g].x *= fix[r], o[r][g].y *= fix[r], o[r][g].z *= fix[r], o[r][g].w *= fix[r];
+      }
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        const int h = kPer * n + kParts + part;
+        __syncwarp();  // the weights are there and the entry before has been read
+        prefetch(h + N - 1);
+        cp_wait<N - 1>();
+        __syncwarp();
+        if (kn.y == 0) continue;
+        const uint8_t *vr = ring + h % N * Y::kEntryBytes;
+        const int dim = kSplit ? 4 * (lane & 15) : 4 * lane;
+#pragma unroll 4
+        for (int i = 0; i < (kSplit ? kTile / 2 : kTile); ++i) {
+          const int k = kSplit ? 2 * i + (lane >> 4) : i;
+          float4 x[kIn];
+#pragma unroll
+          for (int g = 0; g < kIn; ++g) {  // behind d it is whatever was there, in lanes that write nothing
+            const int e = dim + 128 * g;
+            x[g] = load4((const T *)(vr + k * Y::kRowBytes + (((e / kElems) ^ (k & 7)) << 4)) + e % kElems);
+          }
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            const float4 w4 = *(const float4 *)(ps + k * R + r);
+            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+              for (int g = 0; g < kIn; ++g) {
+                float4 &y = o[r + f][part * kIn + g];
+                y.x = fmaf(w[f], x[g].x, y.x);
+                y.y = fmaf(w[f], x[g].y, y.y);
+                y.z = fmaf(w[f], x[g].z, y.z);
+                y.w = fmaf(w[f], x[g].w, y.w);
+              }
+          }
+        }
+      }
+    }
+    // the entry consumed last is free until the next prefetch: it takes this warp's output
+    __syncwarp();
+    float *mine = (float *)(ring + (kPer * n + N - 1) % N * Y::kEntryBytes);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int s = 8; s; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
       if (lane == 0) {
-        wm[row] = m[r];
-        wl[row] = l[r];
+        wm[warp * kMaxRows + r] = m[r];
+        wl[warp * kMaxRows + r] = l[r];
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c4 = q * 128 + lane * 4;
-        if (c4 < d && row < P.R) *(float4 *)(os + row * d + c4) = o[r][q];
+      for (int g = 0; g < kGroups; ++g) {
+        float4 x = o[r][g];
+        if (kSplit) {
+          x.x += __shfl_xor_sync(0xffffffffu, x.x, 16);
+          x.y += __shfl_xor_sync(0xffffffffu, x.y, 16);
+          x.z += __shfl_xor_sync(0xffffffffu, x.z, 16);
+          x.w += __shfl_xor_sync(0xffffffffu, x.w, 16);
+        }
+        const int e = (kSplit ? 4 * (lane & 15) : 4 * lane) + 128 * g;
+        if (e < d && (!kSplit || lane < 16)) *(float4 *)(mine + r * d + e) = x;
       }
     }
-    float *buf[1] = {os};
-    finish_segment<T, 1>(P, L, u, i0, i1, lo, buf, wm, wl);
+    float *buf[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const long long left = i1 - lo - w;  // items of warp w below i1: ceil(left / kWarps)
+      const int nw = left > 0 ? (int)((left + kWarps - 1) / kWarps) : 0;
+      buf[w] = (float *)(smem + w * Y::kWarpBytes + (kPer * nw + N - 1) % N * Y::kEntryBytes);
+    }
+    finish_segment<T, false>(P, L, u, i0, i1, lo, buf, wm, wl);
     settle<T>(P, L, u, i0, i1);
     i0 = i1;
   }
+  cp_wait<0>();
 }
 
 int sm_count() {
@@ -806,16 +890,21 @@ cudaError_t launch_mma(RowsParams &P, cudaStream_t st, bool pdl) {
   return launch_maybe_pdl(k_paged_rows<D, NT>, dim3(P.C), dim3(kThreads), smem, st, pdl, P);
 }
 
-template <typename T>
+template <typename T, int R, int kD_>
 cudaError_t launch_simt(RowsParams &P, cudaStream_t st) {
-  const size_t fixed = (simt_fixed_bytes(P.d) + 15) & ~(size_t)15;
-  const size_t smem = fixed + plan_bytes(P.nb);
-  P.C = min(sm_count() * ctas_per_sm(smem + 4608, 4), kMaxCtas);
-  cudaError_t e = ensure_smem(k_paged_simt<T>, smem);
+  typedef SimtLayout<T, R, kD_> Y;
+  const size_t smem = Y::kOffPlan + plan_bytes(P.nb);
+  P.C = min(sm_count() * ctas_per_sm(smem, Y::kCtas), kMaxCtas);
+  cudaError_t e = ensure_smem(k_paged_simt<T, R, kD_>, smem);
   if (e != cudaSuccess) return e;
   note_launch();
-  k_paged_simt<T><<<P.C, kThreads, smem, st>>>(P, (int)fixed);
+  k_paged_simt<T, R, kD_><<<P.C, kThreads, smem, st>>>(P);
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_simt(RowsParams &P, cudaStream_t st) {
+  if (P.R == 4) return P.d <= 64 ? launch_simt<T, 4, 64>(P, st) : P.d <= 128 ? launch_simt<T, 4, 128>(P, st) : launch_simt<T, 4, 256>(P, st);
+  return P.d <= 64 ? launch_simt<T, 8, 64>(P, st) : P.d <= 128 ? launch_simt<T, 8, 128>(P, st) : launch_simt<T, 8, 256>(P, st);
 }
 
 }  // namespace
@@ -850,7 +939,7 @@ cudaError_t launch_paged_rows(const Dims &D, const Paged &G, const void *q, cons
   P.tpb = (D.B + kTile - 1) / kTile;
   const long long rows = sel ? D.G : std::min((long long)D.G * G.max_chunk, max_rows - 1);
   const bool mma = D.bf16 && (D.d == 64 || D.d == 128 || D.d == 256) && (!sel || D.B % kTile == 0);
-  P.R = mma && rows <= 8 ? 8 : kMaxRows;
+  P.R = mma ? (rows <= 8 ? 8 : 16) : rows <= 4 ? 4 : 8;
   P.rtk = (D.G + P.R - 1) / P.R;
   P.min_items = 2 * kWarps;
   for (P.b0 = 0; P.b0 < G.batch; P.b0 += kMaxSeqs) {

@@ -183,6 +183,17 @@ CASES = [
     ("fp32", 4, 1, 64, 16, 32, 0, [30, 1, 0, 7], [200, 300, 4, 7]),
     ("fp32", 8, 2, 256, 64, 48, 2, [1, 5], [300, 90]),
     ("fp32", 32, 1, 128, 32, 16, 3, [2], [80]),
+    # CUDA cores: streams of many tiles a warp, heads that do not fill their lanes or entries, one to three
+    # 16-byte pieces a row, tiles that cross a page
+    ("fp32", 16, 2, 128, 32, 64, 0, [200, 0, 260], [1500, 10, 1400]),
+    ("fp32", 16, 2, 256, 64, 64, 4, [60, 3], [1500, 1400]),
+    ("fp32", 6, 2, 200, 16, 64, 0, [9, 1, 40], [300, 1, 77]),
+    ("fp32", 4, 4, 136, 16, 24, 5, [9, 1, 40], [300, 1, 77]),
+    ("fp32", 3, 1, 8, 16, 8, 3, [5, 33], [100, 33]),
+    ("bf16", 9, 1, 16, 16, 40, 3, [5, 33], [100, 400]),
+    ("bf16", 8, 2, 72, 32, 64, 0, [5, 33], [100, 400]),
+    ("bf16", 12, 3, 200, 16, 24, 6, [5, 33], [100, 400]),
+    ("bf16", 2, 2, 24, 16, 56, 2, [5, 33], [100, 400]),
 ]
 
 
