@@ -449,17 +449,15 @@ def alloc_paged_workspace(cfg, pg: PagedBatch, device=None) -> torch.Tensor:
 
 
 def _rows(t: torch.Tensor, dtype: torch.dtype, shape, name: str):
-    """(address, row stride) of packed rows: everything behind the first axis is dense."""
+    """(address, row stride) of packed rows [n][heads][d] or [n][d]: everything behind the first axis is dense."""
     if t.dtype != dtype or t.shape != shape:
         _want(t, dtype, shape, name)
-    if not t.is_cuda:
-        raise ValueError("QSA tensors must live on a CUDA device")
-    st, dense = t.stride(), 1
-    for n, stride in zip(shape[:0:-1], st[:0:-1]):
-        if stride != dense and n != 1:
-            raise ValueError(f"{name}: a row's heads must be dense")
-        dense *= n
-    return t.data_ptr(), st[0] if shape[0] > 1 else dense
+    st = t.stride()
+    if (st[-1] != 1 and shape[-1] != 1) or (len(shape) == 3 and st[1] != shape[2] and shape[1] != 1):
+        raise ValueError(f"{name}: a row's heads must be dense")
+    if shape[0] > 1:
+        return t.data_ptr(), st[0]
+    return t.data_ptr(), shape[1] * shape[2] if len(shape) == 3 else shape[1]
 
 
 def _plain(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
@@ -496,10 +494,12 @@ def qsa_norm_rope(cfg, nr: NormRope, pos, q, k, q_out, k_out, stream=None):
     qa = ka = qo = ko = (None, 0)
     if q is not None:
         shape = (n, cfg.num_attention_heads, d)
-        qa, qo = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
+        qa = _rows(q, dt, shape, "q")
+        qo = qa if q_out is q else _rows(q_out, dt, shape, "q_out")
     if k is not None:
         shape = (n, cfg.num_key_value_heads, d)
-        ka, ko = _rows(k, dt, shape, "k"), _rows(k_out, dt, shape, "k_out")
+        ka = _rows(k, dt, shape, "k")
+        ko = ka if k_out is k else _rows(k_out, dt, shape, "k_out")
     _norm_weights(cfg, nr)
     dev = _here(pos, q, k, q_out, k_out, nr.q_weight, nr.k_weight)
     _check(_lib.qsa_norm_rope(ctypes.byref(cfg), ctypes.byref(nr.c), _plain(pos, torch.int32, (n,), "pos"), n, *qa, *qo,
@@ -517,7 +517,8 @@ def qsa_paged_append(cfg, nr: Optional[NormRope], pg: PagedBatch, k, v, k_pages,
     ki_ptr, ki_cap = None, 0
     if q is not None:
         shape = (n, cfg.num_attention_heads, d)
-        qa, qo = _rows(q, dt, shape, "q"), _rows(q_out, dt, shape, "q_out")
+        qa = _rows(q, dt, shape, "q")
+        qo = qa if q_out is q else _rows(q_out, dt, shape, "q_out")
     if ki is not None:
         di = cfg.indexer_head_dim
         ki_cap = ki_cache.shape[1]
