@@ -545,9 +545,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           } else if (valid && have_o) {
-            uint4 *o4 = (uint4 *)(P.part_o + pr * kD + p.hh * 64 + cb * 16);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o4[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+            for (int q = 0; q < 4; ++q)
+              *(uint4 *)(P.part_o + part_at<Two128>(slot, w * kRows + p.row, p.hh * 64 + cb * 16 + 4 * q)) =
+                  make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
           }
         }
       }
