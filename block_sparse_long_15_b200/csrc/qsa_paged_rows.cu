@@ -27,7 +27,7 @@
 // movmatrix per 8 x 8.
 //
 // Measured, 16 / 2 heads of 128, pages of 64: 64 sequences of 4K .. 32K tokens (1.24 GB) 199 us, 6.2 TB/s;
-// over 32 selected blocks each (137 MB) 33 us in a graph, of which the chain of length, list entry, page
+// over 32 selected blocks each (137 MB) 32 us in a graph, of which the chain of length, list entry, page
 // number and first tile takes 6 and the merge of units that CTAs share 2 to 6; one sequence of
 // 1500 tokens 11 us, latency throughout.
 #include <math.h>
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
 // (key, half of the dims) for the logits, whose weights then go through shared memory to lanes that are dims
 // (and, up to 64 dims, halves of the keys). The ring holds K and V of a tile as entries of their own (of up
 // to 512 bytes a row: two each at 256 dims in fp32).
-// Measured in fp32: 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32, 4 / 1 heads of 64, 26 us, latency; a
+// Measured in fp32: 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32, 4 / 1 heads of 64, 23 us in a graph, latency; a
 // step of 64 sequences of 2K .. 8K, 16 / 2 heads of 128, 160 us (4.1 TB/s); 4 chunks of 450 tokens of 2000, 1466 us
 // (17.7 TFLOP/s: shared memory, and the softmax between the products). With 32 keys a step for the whole CTA and
 // barriers around each they took 46, 371 and 1673.

@@ -26,11 +26,11 @@
 //               8K of 32K tokens).
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
 //
-// Measured, 16 / 2 heads, pages of 64: 8192 tokens of 32768 1530 us alone (1.26 PFLOP/s, 0.77 of
-// cuBLAS), 1780 in long loops under the power cap; tensor pipe 60 % busy, MUFU 62 %. A part of the
+// Measured, 16 / 2 heads, pages of 64: 8192 tokens of 32768 1515 us alone (1.27 PFLOP/s, 0.77 of
+// cuBLAS), 1740 in long loops under the power cap; tensor pipe 60 % busy, MUFU 62 %. A part of the
 // exponentials as polynomials on the FMA pipe: no gain, the issue slots are as scarce. 4096 tokens of
-// 24000, 64 independently selected blocks each: 665 us, in which 16 tokens see nearly every
-// block between them and the products of the whole context are made (0.74 PFLOP, 1.1 PFLOP/s). The
+// 24000, 64 independently selected blocks each: 655 us, in which 16 tokens see nearly every
+// block between them and the products of the whole context are made (0.74 TFLOP, 1.1 PFLOP/s). The
 // row kernel, which reads every token's own blocks, is bound by L2 there (1535 us). Products per
 // 64-key half that a tile sees: 675 to 775 us, the shorter MMAs save less than their issue costs.
 #include "qsa_paged_plan.cuh"

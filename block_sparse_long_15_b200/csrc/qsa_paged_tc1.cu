@@ -21,10 +21,10 @@
 // Every wait is bounded; on expiry the kernel records QSA_ERR_TIMEOUT and unwinds.
 //
 // Measured at head_dim 256, 16 / 2 heads: chunks of 1 .. 1500 tokens of 6 sequences (0.53 TFLOP)
-// 510 us, 1.03 PFLOP/s, tensor pipe 52 % busy: the way from S to P (TMEM loads, exponentials, stores,
+// 500 us, 1.05 PFLOP/s, tensor pipe 52 % busy: the way from S to P (TMEM loads, exponentials, stores,
 // two barriers) is longer than the products of one chunk that run beside it. Two groups of softmax
 // warps taking chunks in turn, with the reference passed through shared memory, spilled (96 registers)
-// and took 8 % more. 3 or 4 drafted tokens of 16 sequences of 2K .. 16K (336 MB) 74 us.
+// and took 8 % more. 3 or 4 drafted tokens of 16 sequences of 2K .. 16K (336 MB) 72 us, 69 in a graph.
 #include "qsa_paged_plan.cuh"
 
 namespace qsa {
