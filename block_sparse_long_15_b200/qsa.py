@@ -404,6 +404,10 @@ class NormRope:
         if kinds and kinds[0] != kinds[-1]:
             raise ValueError(f"q_weight and k_weight differ: {kinds[0]} and {kinds[-1]}")
         self.kind = kinds[0] if kinds else None  # dtype and shape, checked against the config in every call
+        devices = [w.get_device() for w in (q_weight, k_weight) if w is not None]
+        if devices and devices[0] != devices[-1]:
+            raise ValueError(f"tensors on {q_weight.device} and {k_weight.device}")
+        self.dev = devices[0] if devices else None
         self.c = qsa_norm_rope_t(eps, weight_offset, rope_theta, rotary_dim, indexer_rotary_dim, _p(q_weight),
                                  _p(k_weight))
 
@@ -423,7 +427,9 @@ class PagedBatch:
         _want_lengths(batch, kv_len=kv_len)
         _want(q_start, torch.int32, (batch + 1,), "q_start")
         _want(page_table, torch.int32, (batch, page_table.shape[1]), "page_table")
-        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        if not q_start.get_device() == kv_len.get_device() == page_table.get_device():
+            raise ValueError(f"tensors on {q_start.device}, {kv_len.device} and {page_table.device}")
+        self.q_start, self.kv_len, self.page_table, self.dev = q_start, kv_len, page_table, kv_len.get_device()
         self.n_tok, self.page_size, self.n_pages = n_tok, page_size, n_pages
         self.c = qsa_paged_t(batch, n_tok, max_chunk, page_size, n_pages, page_table.shape[1], _p(q_start), _p(kv_len),
                              _p(page_table))
@@ -482,9 +488,17 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _norm_weights(cfg, nr: NormRope):
+def _norm_weights(cfg, nr: NormRope, dev: int):
     if nr.kind is not None and nr.kind != (_elem(cfg), (cfg.head_dim,)):
         raise ValueError(f"norm weights: {nr.kind[0]} {tuple(nr.kind[1])}, expected {_elem(cfg)} {(cfg.head_dim,)}")
+    if nr.dev is not None and nr.dev != dev:
+        raise ValueError(f"norm weights on cuda:{nr.dev}, the rows on cuda:{dev}")
+
+
+def _paged_here(pg: PagedBatch, *tensors) -> int:
+    if pg.dev != _here(*tensors):
+        raise ValueError(f"the batch is on cuda:{pg.dev}, the rows on {tensors[0].device}")
+    return pg.dev
 
 
 def qsa_norm_rope(cfg, nr: NormRope, pos, q, k, q_out, k_out, stream=None):
@@ -500,8 +514,8 @@ def qsa_norm_rope(cfg, nr: NormRope, pos, q, k, q_out, k_out, stream=None):
         shape = (n, cfg.num_key_value_heads, d)
         ka = _rows(k, dt, shape, "k")
         ko = ka if k_out is k else _rows(k_out, dt, shape, "k_out")
-    _norm_weights(cfg, nr)
-    dev = _here(pos, q, k, q_out, k_out, nr.q_weight, nr.k_weight)
+    dev = _here(pos, q, k, q_out, k_out)
+    _norm_weights(cfg, nr, dev)
     _check(_lib.qsa_norm_rope(ctypes.byref(cfg), ctypes.byref(nr.c), _plain(pos, torch.int32, (n,), "pos"), n, *qa, *qo,
                               *ka, *ko, _raw_stream(stream, dev)), "qsa_norm_rope")
 
@@ -524,10 +538,9 @@ def qsa_paged_append(cfg, nr: Optional[NormRope], pg: PagedBatch, k, v, k_pages,
         ki_cap = ki_cache.shape[1]
         kia = _rows(ki, dt, (n, di), "ki")
         ki_ptr = _plain(ki_cache, dt, (pg.c.batch, ki_cap, di), "ki_cache")
+    dev = _paged_here(pg, k, v, k_pages, v_pages, workspace, q, q_out, ki, ki_cache)
     if nr is not None:
-        _norm_weights(cfg, nr)
-        _here(k, nr.q_weight, nr.k_weight)
-    dev = _here(k, v, k_pages, v_pages, workspace, q, q_out, ki, ki_cache, pg.q_start, pg.kv_len, pg.page_table)
+        _norm_weights(cfg, nr, dev)
     t = qsa_append_t(ka[0], va[0], ka[1], va[1], _plain(k_pages, dt, pool, "k_pages"), _plain(v_pages, dt, pool, "v_pages"),
                      *qa, *qo, *kia, ki_ptr, ki_cap)
     _check(_lib.qsa_paged_append(ctypes.byref(cfg), ctypes.byref(nr.c) if nr is not None else None, ctypes.byref(pg.c),
@@ -543,7 +556,7 @@ def qsa_paged_attn(cfg, pg: PagedBatch, q, k_pages, v_pages, sel, out, workspace
     sel_ptr = None
     if sel is not None:
         sel_ptr = _plain(sel, torch.int32, (n, qsa_topk_blocks(cfg)), "sel")
-    dev = _here(q, k_pages, v_pages, sel, out, workspace, pg.q_start, pg.kv_len, pg.page_table)
+    dev = _paged_here(pg, q, k_pages, v_pages, sel, out, workspace)
     _check(_lib.qsa_paged_attn(ctypes.byref(cfg), ctypes.byref(pg.c), _plain(q, dt, rows, "q"),
                                _plain(k_pages, dt, pool, "k_pages"), _plain(v_pages, dt, pool, "v_pages"), sel_ptr,
                                _plain(out, dt, rows, "out"), _p(workspace), workspace.numel(), _raw_stream(stream, dev)),
