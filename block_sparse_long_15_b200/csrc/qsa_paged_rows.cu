@@ -90,12 +90,14 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
 // Every CTA for itself: items per sequence and their prefix sums.
 __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
   __shared__ long long s_sum[kWarps];
+  __shared__ int s_max[kWarps];
   L.pre = (long long *)smem;
   L.seq = (SeqItems *)(smem + (size_t)(P.nb + 1) * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (P.nb + kThreads - 1) / kThreads;
   const int a = min(P.nb, (int)threadIdx.x * per), z = min(P.nb, a + per);
   long long run = 0;
+  int most = 0;  // tiles of a unit
   for (int b = a; b < z; ++b) {
     PagedSeq s = paged_seq(P.P, P.b0 + b, P.status);
     if ((long long)s.n * P.G >= P.max_rows) s.n = 0;
@@ -110,6 +112,7 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
       tiles = (s.len + kTile - 1) / kTile;
     }
     L.seq[b] = {s.q0, s.n, s.len, rt, tiles};
+    if (rt > 0) most = max(most, tiles);
     run += (long long)rt * tiles * P.Hkv;
     L.pre[b + 1] = run;
   }
@@ -120,14 +123,22 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_sum[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) s_max[warp] = most;
   if (threadIdx.x == 0) L.pre[0] = 0;
   __syncthreads();
   long long before = incl - run;
   for (int w = 0; w < warp; ++w) before += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) most = max(most, s_max[w]);
   for (int b = a; b < z; ++b) L.pre[b + 1] += before;
   __syncthreads();
   L.T = L.pre[P.nb];
-  L.C = (int)min((long long)P.C, div_pos(L.T + P.min_items - 1, P.min_items));
+  // A CTA should have as many items as make it worth having, and where few units are long, more: with n tiles
+  // in a unit and i of them a CTA, streaming takes about i / 8 us and the merge of its n / i parts n / 10 i.
+  // One sequence of 16000, 16 / 2 heads of 128, in a graph: 18 us, 32 with 8 items a CTA; two tokens of it 27 and
+  // 58; of 8 KV heads, which fill the device with less, 20 and 17.
+  const int items = max(P.min_items, (int)sqrtf(0.8f * (float)most));
+  L.C = (int)min((long long)P.C, div_pos(L.T + items - 1, items));
 }
 
 // CTA of item i: floor(c T / C) <= i < floor((c + 1) T / C)
