@@ -179,6 +179,10 @@ class QSAPaged:
 
     def reserve(self, counts):
         """Room for counts[s] more tokens of every slot s: for all of them or, with an error, for none."""
+        self._take(counts, self._room(counts))
+
+    def _room(self, counts):
+        """Pages that counts[s] more tokens need in every slot s, or an error where there is no room."""
         if len(counts) != self.slots:
             raise ValueError(f"{len(counts)} counts for {self.slots} slots")
         need = []
@@ -188,11 +192,21 @@ class QSAPaged:
             need.append(-(-(self.length[s] + n) // self.page_size) - len(self.pages[s]))
         if sum(need) > len(self.free):
             raise ValueError(f"{sum(need)} pages needed, {len(self.free)} free")
+        return need
+
+    def _take(self, counts, need):
         for s, (n, m) in enumerate(zip(counts, need)):
             for _ in range(m):
                 self.table[s, len(self.pages[s])] = self.free[-1]
                 self.pages[s].append(self.free.pop())
             self.length[s] += n
+
+    def _give_back(self, counts, need):
+        """_take undone, with the free pages in the order that they had."""
+        for s in reversed(range(self.slots)):
+            for _ in range(need[s]):
+                self.free.append(self.pages[s].pop())
+            self.length[s] -= counts[s]
 
     def batch(self, counts):
         """The packed batch of counts[s] new tokens of every slot, whose lengths count them already."""
@@ -205,8 +219,10 @@ class QSAPaged:
         """Selection [n_tok][k] of the packed rows qi [n_tok][Hi][di]: compresses the blocks that the step
         completed, then scores and selects with every slot's rows padded to the longest chunk."""
         cfg, most = self.cfg, max(counts)
+        done = self.kbar_blocks.clone()  # a tensor of its own: a step that is refused later takes the old one back
         qsa.qsa_compress_blocks(cfg, self.ki_cache, self.kv_start, pg.kv_len, self.kbar_cache,
-                                blocks_done=self.kbar_blocks.clone(), kbar_blocks=self.kbar_blocks)
+                                blocks_done=self.kbar_blocks, kbar_blocks=done)
+        self.kbar_blocks = done
         count = torch.tensor(counts)
         seq = torch.repeat_interleave(torch.arange(self.slots), count).to(self.device)
         row = torch.cat([torch.arange(c) for c in counts]).to(self.device)
@@ -223,6 +239,7 @@ class QSAPaged:
         [n_tok][Hkv][d] before norm and rotation. With the indexer's qi [n_tok][Hi][di] (rotated) and ki
         [n_tok][di] the step attends the selected blocks; a slot whose earlier tokens came without them
         cannot. Returns [n_tok][Hq][d]."""
+        need = self._room(counts)
         cfg, n = self.cfg, sum(counts)
         heads, kv = (n, cfg.num_attention_heads, cfg.head_dim), (n, cfg.num_key_value_heads, cfg.head_dim)
         want = [("q", q, heads), ("k", k, kv), ("v", v, kv)]
@@ -233,21 +250,30 @@ class QSAPaged:
             for s, c in enumerate(counts):
                 if c and self.indexed[s] != self.length[s]:
                     raise ValueError(f"slot {s}: {self.length[s]} tokens, {self.indexed[s]} of them with indexer keys")
-        for name, t, shape in want:  # before the lengths move
+        for name, t, shape in want:
             if tuple(t.shape) != shape or t.dtype != self.dtype:
                 raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} {self.dtype}")
-        self.reserve(counts)
         if n == 0:
             return torch.empty_like(q)
-        pg = self.batch(counts)
-        self.ws = self._grown(self.ws, qsa.qsa_paged_workspace_size(self.cfg, pg))
+        # Any of the calls below may still refuse (strides, alignment, devices, norm weights, sizes that no
+        # kernel serves): the slots are then as they were. What the calls before it wrote lies behind the slots'
+        # tokens, where the next step writes again.
+        blocks = self.kbar_blocks
+        self._take(counts, need)
+        try:
+            pg = self.batch(counts)
+            self.ws = self._grown(self.ws, qsa.qsa_paged_workspace_size(cfg, pg))
+            turned, out = torch.empty_like(q), torch.empty_like(q)
+            qsa.qsa_paged_append(cfg, self.nr, pg, k, v, self.k_pages, self.v_pages, self.ws, q=q, q_out=turned, ki=ki,
+                                 ki_cache=self.ki_cache if ki is not None else None)
+            sel = self.select(counts, qi, pg) if ki is not None else None
+            qsa.qsa_paged_attn(cfg, pg, turned, self.k_pages, self.v_pages, sel, out, self.ws)
+        except BaseException:
+            self._give_back(counts, need)
+            self.kbar_blocks = blocks
+            raise
         if ki is not None:
             self.indexed = [a + c for a, c in zip(self.indexed, counts)]
-        turned, out = torch.empty_like(q), torch.empty_like(q)
-        qsa.qsa_paged_append(self.cfg, self.nr, pg, k, v, self.k_pages, self.v_pages, self.ws, q=q, q_out=turned, ki=ki,
-                             ki_cache=self.ki_cache if ki is not None else None)
-        sel = self.select(counts, qi, pg) if ki is not None else None
-        qsa.qsa_paged_attn(self.cfg, pg, turned, self.k_pages, self.v_pages, sel, out, self.ws)
         return out
 
     def _grown(self, ws, need: int):
