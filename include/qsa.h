@@ -325,11 +325,19 @@ qsa_status_t qsa_decode_offload(const qsa_config_t *cfg, const qsa_tensors_t *t,
  * Serving from a paged cache. A serving process holds the K/V cache in pages that
  * its sequences share out among themselves, and runs a batch of sequences with a
  * few new tokens each: one for a decode step, some for drafted tokens, many for a
- * chunk of a prompt. A step is qsa_project (with q_first all zero, where its rotation
- * is the identity), qsa_paged_append, then, on a layer with QSA, qsa_compress_blocks
- * and qsa_index_score_topk on the indexer's own cache (which stays one plane per
- * sequence), and qsa_paged_attn over the pages. (The model page has paged caches
- * nowhere; the layouts here are this library's.)
+ * chunk of a prompt. A step is qsa_project with every packed token as a sequence of its
+ * own (below), qsa_paged_append, then, on a layer with QSA, qsa_norm_rope for the rotation
+ * of qi, qsa_compress_blocks and qsa_index_score_topk on the indexer's own cache (which
+ * stays one plane per sequence), and qsa_paged_attn over the pages. (The model page has
+ * paged caches nowhere; the layouts here are this library's.)
+ *
+ * qsa_project's part: batch = the packed tokens, n_tok = 1, kv_cap = 1, kv_row0 = 0. q, qi,
+ * k, v and ki then come out as the packed rows that the calls here take, and q_first holds
+ * a position for every token. It is 0 for all of them: the rotation is the identity there,
+ * and the append rotates. (A chunk given as ONE sequence would be rotated at 0, 1, 2 ..
+ * there and at its positions here, and its k and v come out head by head.) Where keys and
+ * queries are not normed and the projection's fp32 angles will do, q_first may hold the
+ * tokens' positions instead, and the append is called with nr NULL.
  *
  * The batch is packed: the new tokens of sequence b are rows q_start[b] ..
  * q_start[b + 1] - 1 of every packed tensor, and with n = q_start[b + 1] -
