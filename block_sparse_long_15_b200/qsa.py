@@ -415,7 +415,8 @@ class NormRope:
 def make_norm_rope(q_weight=None, k_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
                    rope_theta: float = 1e4, rotary_dim: int = 0, indexer_rotary_dim: int = 0) -> NormRope:
     """q_weight / k_weight: [head_dim] of the config's dtype; None leaves that side without the norm.
-    weight_offset=1.0 for weights stored around zero; rotary_dim=0 for no rotation."""
+    weight_offset=1.0 for weights stored around zero; rotary_dim=0 for no rotation, else
+    rope_theta is 1 .. 3e38."""
     return NormRope(q_weight, k_weight, eps, weight_offset, rope_theta, rotary_dim, indexer_rotary_dim)
 
 

@@ -379,7 +379,7 @@ typedef struct {
 typedef struct {
   float eps;                  /* >= 0 */
   float weight_offset;
-  float rope_theta;           /* > 0 where something rotates */
+  float rope_theta;           /* 1 .. 3e38 where something rotates (else QSA_ERR_INVALID_ARG) */
   int32_t rotary_dim;         /* multiple of 16, <= head_dim; 0: q and k do not rotate */
   int32_t indexer_rotary_dim; /* multiple of 16, <= indexer_head_dim; 0: ki does not rotate */
   const void *q_weight;       /* [d] of cfg->dtype, device memory; NULL: queries are not normed */
