@@ -526,7 +526,7 @@ qsa_status_t resolve_norm_rope(const Dims &D, const qsa_norm_rope_t *nr, NormRop
   if (!aligned16(nr->q_weight) || !aligned16(nr->k_weight)) return QSA_ERR_INVALID_ARG;
   N->eps = nr->eps;
   N->w_off = nr->weight_offset;
-  N->log2_theta = nr->rotary_dim || nr->indexer_rotary_dim ? log2((double)nr->rope_theta) : 0.0;
+  N->log2_theta = nr->rotary_dim || nr->indexer_rotary_dim ? log2l(nr->rope_theta) : 0.0L;
   N->rot = nr->rotary_dim;
   N->rot_i = nr->indexer_rotary_dim;
   N->qw = nr->q_weight;

@@ -242,7 +242,7 @@ cudaError_t launch_validate_paged_sel(const Dims &D, const Paged &P, const int32
 // pos takes each row's position from the paged batch.
 struct NormRope {
   float eps, w_off;
-  double log2_theta;
+  long double log2_theta;
   int rot, rot_i;
   const void *qw, *kw;
 };
