@@ -542,7 +542,8 @@ int chunk_rows(const Dims &D, bool sel) { return sel ? 12 * D.G : D.d == 256 ? 9
 // With one, it reads every token's own blocks, while a tile reads the union of its tokens': with
 // independent selections of 2048 keys and 2 KV heads of 128 the row kernel takes 41 us for 4 chunks
 // of 32 tokens, 120 for 16 and 233 for 32, the tensor-core kernel 64, 102 and 144; 32 chunks of 8
-// tokens 75 and 130.
+// tokens 75 and 130. The rule counts the keys that the row kernel reads. It does not know how much of the
+// context the tokens' lists cover between them, on which a tile's time depends, and was measured with groups of 8.
 bool use_paged_tc(const Dims &D, const Paged &G, bool sel) {
   if ((long long)G.max_chunk * D.G < chunk_rows(D, sel) || !paged_tc_supported(D, G, sel)) return false;
   return !sel || (long long)G.n_tok * D.Hkv * D.d * D.k * D.B >= 1LL << 28;

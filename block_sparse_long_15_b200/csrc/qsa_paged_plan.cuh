@@ -238,7 +238,10 @@ __device__ __forceinline__ bool idle_wait_warp(uint64_t *bar, uint32_t parity) {
 
 // P for keys kFrom .. kTo - 1 of 32 held in registers (fp32 bits), written back in place over
 // sv[kFrom / 2 ..] as bf16 pairs: p = 2^(s * scale - m) for keys below `lim`, 0 from there on. Adds
-// them to acc (the fp32 values: only the product with V sees them in bf16).
+// them to acc (the fp32 values: only the product with V sees them in bf16, since both operands of an
+// MMA have one type and V is bf16). Outputs are 2.3e-3 from the 64-bit form (2-norm), 1.7e-3 of it
+// their own rounding to bf16; a second product with P's low half would take the MMAs of a chunk from two to three
+// parts, where the tensor pipe is busy 60 % of the time already.
 template <bool kAll, int kFrom = 0, int kTo = 32>
 __device__ __forceinline__ void p_quarter(uint32_t (&sv)[32], int lim, uint64_t scale2, uint64_t negm2, uint64_t (&acc)[2]) {
 #pragma unroll
@@ -389,7 +392,7 @@ __device__ __forceinline__ size_t part_at(int slot, int row, int col) {
 // Block (c, y, z): rows 32 y .. of the unit that begins in CTA c's range and goes on in later ones, 128
 // elements of each from 128 z on. A lane is a row, a warp 8 elements of it:
 //   out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
-// With cold caches 7.5 us behind drafted tokens of 16 sequences, 20 behind 148 long ranges (78 MB of parts).
+// With cold caches 7.5 us behind drafted tokens of 16 sequences, 20 behind 148 long ranges (39 MB of parts).
 constexpr int kMergeWarps = 16, kMergeRows = 32, kMergeParts = 8;
 template <class X>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {

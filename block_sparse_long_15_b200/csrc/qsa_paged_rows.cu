@@ -134,9 +134,10 @@ __device__ void make_plan(const RowsParams &P, uint8_t *smem, Plan &L) {
   __syncthreads();
   L.T = L.pre[P.nb];
   // A CTA should have as many items as make it worth having, and where few units are long, more: with n tiles
-  // in a unit and i of them a CTA, streaming takes about i / 8 us and the merge of its n / i parts n / 10 i.
-  // One sequence of 16000, 16 / 2 heads of 128, in a graph: 18 us, 32 with 8 items a CTA; two tokens of it 27 and
-  // 58; of 8 KV heads, which fill the device with less, 20 and 17.
+  // in a unit and i of them a CTA, streaming takes about i / 8 us and the merge of its n / i parts, which its
+  // last CTA makes alone, n / 10 i. The rule goes by the longest unit of the batch and not by how many there are.
+  // One sequence of 16000, 16 / 2 heads of 128, in a graph: 18.5 us, 32 with 8 items a CTA; two tokens of it 27 and
+  // 58; of 8 KV heads, which fill the device without it, 20 and 17.
   const int items = max(P.min_items, (int)sqrtf(0.8f * (float)most));
   L.C = (int)min((long long)P.C, div_pos(L.T + items - 1, items));
 }
@@ -542,7 +543,11 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
           x[e] = p0;
           x[e + 2] = p1;
         }
-        // P in bf16 for the product; its sum stays in fp32 of the unrounded values
+        // P in bf16 for the product, whose operands have one type (V is bf16); its sum stays in fp32 of the
+        // unrounded values. Outputs are 2.3e-3 from the 64-bit form (2-norm), 1.7e-3 of it their own rounding to
+        // bf16. A second product with P's low half leaves the 1.7e-3 and takes 203.2 us instead of 200.6 at 64
+        // sequences of 4K .. 32K, 33.2 instead of 32.8 over selected blocks; the other attention kernels of this
+        // library round P too.
         pb[nt][0] = transpose8x8(pack_bf16x2(x[0], x[1]));
         pb[nt][1] = transpose8x8(pack_bf16x2(x[2], x[3]));
       }
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_rows(const __grid_constant__
 // (and, up to 64 dims, halves of the keys). The ring holds K and V of a tile as entries of their own (of up
 // to 512 bytes a row: two each at 256 dims in fp32).
 // Measured in fp32: 3 chunks of 60 .. 256 tokens over 4 selected blocks of 32, 4 / 1 heads of 64, 23 us in a graph, latency; a
-// step of 64 sequences of 2K .. 8K, 16 / 2 heads of 128, 160 us (4.1 TB/s); 4 chunks of 450 tokens of 2000, 1466 us
+// step of 64 sequences of 2K .. 8K, 16 / 2 heads of 128, 162 us (4.1 TB/s); 4 chunks of 450 tokens of 2000, 1474 us
 // (17.7 TFLOP/s: shared memory, and the softmax between the products). With 32 keys a step for the whole CTA and
 // barriers around each they took 46, 371 and 1673.
 template <typename T, int R, int kD_>
@@ -622,12 +627,10 @@ struct SimtLayout {
   static constexpr int kElems = 16 / sizeof(T);  // elements of 16 bytes
   static constexpr int kPart = kD_ * sizeof(T) <= 512 ? kD_ : 512 / sizeof(T), kParts = kD_ / kPart;  // dims of an entry
   static constexpr uint32_t kRowBytes = kPart * sizeof(T), kEntryBytes = kTile * kRowBytes;
-  // Few entries and many warps: at 128 dims in fp32 two entries and three CTAs an SM take 1466 us where three
-  // entries and two CTAs take 1873 (four chunks of 450 tokens of 2000, 16 / 2 heads), at 64 dims three
-  // and four take 27 us where four and three take 29 (the small case above).
   // Few entries and many warps: the logits and the softmax of a tile are one chain, which other warps cover. In
   // fp32, four chunks of 450 tokens of 2000, 16 / 2 heads: at 128 dims two entries and three CTAs an SM
-  // 1466 us, three and two 1873; at 256 dims 3088 and 3552.
+  // 1474 us, three and two 1889; at 256 dims 3102 and 3583. At 64 dims three and four take 22.7 us for the small
+  // case above and 978 for these chunks, four and three 24.6 and 899.
   static constexpr int kEntries = kRowBytes <= 256 ? 3 : 2;
   static constexpr int kCtas = kRowBytes <= 256 ? 4 : 3;  // per SM
   static constexpr uint32_t kWarpBytes = kEntries * kEntryBytes;

@@ -178,7 +178,9 @@ class QSAPaged:
         self.kbar_blocks[slot] = 0
 
     def reserve(self, counts):
-        """Room for counts[s] more tokens of every slot s: for all of them or, with an error, for none."""
+        """Room for counts[s] more tokens of every slot s: for all of them or, with an error, for none. The lengths
+        count them from here on: the caller appends them itself (batch, qsa.qsa_paged_append). A step needs no
+        call of this, it reserves its own."""
         self._take(counts, self._room(counts))
 
     def _room(self, counts):
@@ -217,7 +219,8 @@ class QSAPaged:
 
     def select(self, counts, qi, pg):
         """Selection [n_tok][k] of the packed rows qi [n_tok][Hi][di]: compresses the blocks that the step
-        completed, then scores and selects with every slot's rows padded to the longest chunk."""
+        completed, then scores and selects with every slot's rows padded to the longest chunk (slots * max(counts)
+        rows of indexer queries and lists, whatever n_tok is)."""
         cfg, most = self.cfg, max(counts)
         done = self.kbar_blocks.clone()  # a tensor of its own: a step that is refused later takes the old one back
         qsa.qsa_compress_blocks(cfg, self.ki_cache, self.kv_start, pg.kv_len, self.kbar_cache,
@@ -238,7 +241,8 @@ class QSAPaged:
         """counts[s] new tokens of every slot s, packed in that order: q [n_tok][Hq][d] and k, v
         [n_tok][Hkv][d] before norm and rotation. With the indexer's qi [n_tok][Hi][di] (rotated) and ki
         [n_tok][di] the step attends the selected blocks; a slot whose earlier tokens came without them
-        cannot. Returns [n_tok][Hq][d]."""
+        cannot. Returns [n_tok][Hq][d]. A step that raises leaves the slots as they were. It copies geometry and
+        page table from the host, so it cannot be captured into a graph; the calls that it makes can."""
         need = self._room(counts)
         cfg, n = self.cfg, sum(counts)
         heads, kv = (n, cfg.num_attention_heads, cfg.head_dim), (n, cfg.num_key_value_heads, cfg.head_dim)

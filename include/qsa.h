@@ -429,12 +429,13 @@ qsa_status_t qsa_paged_append(const qsa_config_t *cfg, const qsa_norm_rope_t *nr
 qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t *pg, size_t *bytes);
 
 /* Attention of the batch's new tokens over the paged cache, their own keys and values
- * included: q, out [n_tok][Hq][d] (dense, not overlapping). With sel NULL a row at position t attends
- * every token u <= t (a full-attention layer without the indexer). With sel [n_tok][k],
- * as qsa_index_score_topk writes it for the rows, it attends the listed blocks below
- * n_c(t) and its trailing range [n_c B, t], as in qsa_sparse_attn; a row that sees no
- * token is written as zeros. Accumulation is fp32; outputs are rounded once at the end.
- * The result does not depend on the batch's order of execution: equal calls give equal
+ * included: q, out [n_tok][Hq][d] (dense, not overlapping). With sel NULL a row at
+ * position t attends every token u <= t (a full-attention layer without the indexer). With
+ * sel [n_tok][k], as qsa_index_score_topk writes it for the rows (ascending, no id twice,
+ * then -1), it attends the listed blocks below n_c(t) and its trailing range [n_c B, t], as
+ * in qsa_sparse_attn; a row that sees no token is written as zeros. Accumulation is fp32;
+ * with bf16 inputs the probabilities are rounded to bf16 for the product with V, as in the
+ * other attention calls; outputs are rounded once at the end. The result does not depend on the batch's order of execution: equal calls give equal
  * bits. */
 qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, const void *q, const void *k_pages,
                             const void *v_pages, const int32_t *sel, void *out, void *workspace,
