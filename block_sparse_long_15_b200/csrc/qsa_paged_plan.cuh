@@ -392,7 +392,7 @@ __device__ __forceinline__ size_t part_at(int slot, int row, int col) {
 // Block (c, y, z): rows 32 y .. of the unit that begins in CTA c's range and goes on in later ones, 128
 // elements of each from 128 z on. A lane is a row, a warp 8 elements of it:
 //   out = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
-// With cold caches 7.5 us behind drafted tokens of 16 sequences, 20 behind 148 long ranges (39 MB of parts).
+// With cold caches 9 us behind drafted tokens of 16 sequences, 22 behind 148 long ranges (39 MB of parts).
 constexpr int kMergeWarps = 16, kMergeRows = 32, kMergeParts = 8;
 template <class X>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const __grid_constant__ TcParams P) {
