@@ -435,8 +435,10 @@ qsa_status_t qsa_paged_workspace_size(const qsa_config_t *cfg, const qsa_paged_t
  * then -1), it attends the listed blocks below n_c(t) and its trailing range [n_c B, t], as
  * in qsa_sparse_attn; a row that sees no token is written as zeros. Accumulation is fp32;
  * with bf16 inputs the probabilities are rounded to bf16 for the product with V, as in the
- * other attention calls; outputs are rounded once at the end. The result does not depend on the batch's order of execution: equal calls give equal
- * bits. */
+ * other attention calls; outputs are rounded once at the end. The result does not depend on
+ * the batch's order of execution: equal calls give equal bits. (Device waits are bounded at
+ * 2 s: a chunk whose tokens see more than about 1e8 keys each, which one SM streams for as
+ * long, records QSA_ERR_TIMEOUT.) */
 qsa_status_t qsa_paged_attn(const qsa_config_t *cfg, const qsa_paged_t *pg, const void *q, const void *k_pages,
                             const void *v_pages, const int32_t *sel, void *out, void *workspace,
                             size_t workspace_bytes, qsa_stream_t stream);
